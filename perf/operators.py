@@ -294,7 +294,7 @@ def run(s):
         call = moe.moe_grouped_gemm if op == "gemm" else moe.moe_grouped_gemm_dx
         return call(s["x"] if op == "gemm" else s["dy"], s["w"], s["offsets"],
                     sorted_ids=s["sorted_ids"] if gather or scatter else None, topk=s["topk"],
-                    gather=gather, scatter=scatter)
+                    num_tokens=s["T"], gather=gather, scatter=scatter)
     if op == "silu":
         return _plain_silu(s)
     if op == "norm":
