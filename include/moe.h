@@ -388,6 +388,158 @@ moe_status moe_fused_forward_noalloc(const void *x, const void *w_router,
                                      int M, int K, int N, int E, int topk, void *out,
                                      void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The layer in pieces, with gradients: for callers that train it, or that put
+ * something between its steps.  A forward pass is
+ *
+ *   h, u  = moe_block_norm(...)                  the norm before the block
+ *   ids, wts = moe_topk(u, ...);  sorted_ids, expert_offsets = moe_align(ids, ...)
+ *   g = moe_grouped_gemm(u, w1, gather)          [R,2N], expert-sorted rows
+ *   a = moe_silu_mul(g, wts)                     [R,N], times the routing weight
+ *   o = moe_grouped_gemm(a, w2, scatter)         [M*topk,K], rows in slot order
+ *   h', u' = moe_block_norm(h, o, ...)           sums a token's slots, norm after
+ *                                                the block, gate, residual, next norm
+ *
+ * and the backward pass the same calls' gradients in reverse.  (The pages
+ * describe the fused forward only; these entry points are not on them.)
+ *
+ * Sorted rows.  Row i of the R sorted rows belongs to the expert e whose range
+ * expert_offsets[e] <= i < expert_offsets[e+1] holds it (moe_align's output;
+ * block_m = 1 gives ranges without padding).  sorted_ids[i] is the row's slot
+ * p = t*topk + j; a value outside [0, T*topk) marks a padding row, which
+ * counts as a row of zeros wherever it is read.  Rows in no range are not
+ * read, and no output row is written for them.  Offsets are clamped to [0,R]
+ * on the device, so none takes an access out of bounds; a list that is not
+ * ascending gives unspecified results.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    MOE_ROWS_SORTED = 0,    /* operand row i is sorted row i */
+    MOE_ROWS_GATHER = 1,    /* the input (moe_grouped_gemm_dw: x) has T rows; sorted row i
+                               reads row sorted_ids[i] / topk */
+    MOE_ROWS_SCATTER = 2,   /* the output has T*topk rows; sorted row i writes row
+                               sorted_ids[i], padding rows write nothing */
+    MOE_ROWS_GATHER_DY = 4  /* moe_grouped_gemm_dw: dy has T rows, read as x above */
+} moe_rows;
+
+typedef enum {
+    MOE_OUT_BF16 = 0,
+    MOE_OUT_FP32 = 1,
+    MOE_OUT_FP32_ADD = 2    /* fp32, added to what the buffer holds */
+} moe_out;
+
+/*
+ * moe_grouped_gemm / _dx / _dw -- matrix products grouped by expert with
+ * ragged row ranges, and their gradients; fp32 accumulation, each output
+ * value rounded once.
+ *
+ *   moe_grouped_gemm     y[i,n]  = sum_k w[e,n,k] x[i,k]
+ *   moe_grouped_gemm_dx  dx[i,k] = sum_n w[e,n,k] dy[i,n]
+ *   moe_grouped_gemm_dw  dw[e,n,k] = sum over e's rows i of dy[i,n] x[i,k];
+ *                        zeros (nothing added) for an expert without rows
+ *
+ *   x, dy           bf16 rows of K and of N values: R rows, or T (GATHER...)
+ *   w               bf16 [E,N,K]
+ *   expert_offsets  int32 [E+1]
+ *   sorted_ids      int32 [R], or NULL: no padding rows, `rows` 0
+ *   rows            moe_rows bits
+ *   T, topk         tokens and slots a token; used with sorted_ids only
+ *   y, dx           out bf16 rows of N and of K values: R rows, or T*topk
+ *                   (SCATTER; rows of slots that sorted_ids does not name stay
+ *                   as they are, a slot named twice gets one of the two).
+ *                   Without SCATTER a padding row inside a range is written
+ *                   as zeros.
+ *   out, dw         moe_out; out [E,N,K] bf16 or fp32
+ *   workspace       as moe_align_ex (moe_grouped_gemm_dw); the size depends on
+ *                   (rows, T, topk, R, E, K, N, out) only
+ *
+ * Results do not depend on scheduling: every sum has a fixed order.  R == 0
+ * is a no-op for y and dx; dw is written (or left, FP32_ADD).
+ *
+ * Errors: INVALID_ARG for null or misaligned pointers, negative sizes,
+ * topk < 1, unknown bits in `rows`, bits without sorted_ids, an unknown `out`;
+ * UNSUPPORTED for E > 256, topk > 16, R or T*topk >= 2^28, K or N >= 2^20,
+ * N*K*2 >= 2^31 (one expert's weights), a gathered operand of 2^31 bytes or
+ * more, or more than 2^31 output tiles of 64 x 64; WORKSPACE.
+ */
+moe_status moe_grouped_gemm(const void *x, const void *w, const int32_t *expert_offsets,
+                            const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
+                            int K, int N, void *y, void *stream);
+moe_status moe_grouped_gemm_dx(const void *dy, const void *w, const int32_t *expert_offsets,
+                               const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
+                               int K, int N, void *dx, void *stream);
+moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *expert_offsets,
+                               const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
+                               int K, int N, int out, void *dw, void *workspace,
+                               size_t *workspace_bytes, void *stream);
+
+/*
+ * moe_silu_mul / _bwd -- the gated activation between the two products with
+ * the row's routing weight, and its gradients:
+ *
+ *   a[i,n]  = wt[p] * silu(g[i,n]) * g[i,N+n],   p = sorted_ids[i]
+ *   dg      = the gradient of g, both halves;  dtopk_weights[p] = sum_n
+ *             da[i,n] silu(g[i,n]) g[i,N+n]
+ *
+ *   g              bf16 [R,2N]: gate values, then up values
+ *   topk_weights   fp32 [slots], or NULL: 1 for every row
+ *   sorted_ids     int32 [R], or NULL: row i is slot i (slots >= R with weights)
+ *   num_rows       device int32 [1] (moe_align's num_padded), or NULL: rows at
+ *                  and past it stay as they are
+ *   a, da          bf16 [R,N];  dg  bf16 [R,2N]
+ *   dtopk_weights  out fp32 [slots], or NULL; slots that no row names stay as
+ *                  they are
+ *
+ * Padding rows are written as zeros.  Errors: INVALID_ARG for null or
+ * misaligned pointers, negative sizes, fewer slots than rows without
+ * sorted_ids, dtopk_weights without topk_weights; UNSUPPORTED for R or slots
+ * >= 2^28 or N >= 2^20.
+ */
+moe_status moe_silu_mul(const void *g, const float *topk_weights, const int32_t *sorted_ids,
+                        const int32_t *num_rows, int slots, int R, int N, void *a, void *stream);
+moe_status moe_silu_mul_bwd(const void *da, const void *g, const float *topk_weights,
+                            const int32_t *sorted_ids, const int32_t *num_rows, int slots, int R,
+                            int N, void *dg, float *dtopk_weights, void *stream);
+
+/*
+ * moe_block_norm / _bwd -- the norms after and before a block with the
+ * block's gate and residual scale, rms(v)^2 = mean(v^2) + eps:
+ *
+ *   s  = sum_j o[t*topk + j]
+ *   h_out = h + res_scale * gate[t] * (w_post ? s / rms(s) * w_post : s)
+ *   u  = h_out / rms(h_out) * w_pre
+ *
+ *   h, h_out    [M,K], bf16 or fp32 (h_dtype: MOE_OUT_BF16 / MOE_OUT_FP32);
+ *               h_out may be h
+ *   o           bf16 [M*topk,K], a token's slots one after the other, or NULL:
+ *               no block before this norm (gate, w_post, h_out NULL; u = the
+ *               norm of h)
+ *   gate        fp32 [M], or NULL: 1
+ *   w_post      fp32 [K], or NULL: the block's output without a norm
+ *   w_pre, u    fp32 [K] and out bf16 [M,K], or both NULL: no norm after
+ *   rstd_post, rstd_pre  out fp32 [M]: 1 / rms, for the backward, or NULL
+ *
+ * Backward: dh_out [M,K] in h's type (or NULL) and du bf16 [M*du_topk,K], a
+ * token's rows summed (NULL iff w_pre is), give dh [M,K] in h's type, d_o
+ * bf16 [M,K] (the gradient of every slot of the token), dgate [M], dw_post
+ * [K], dw_pre [K] (fp32, each asked for iff its input is given).  Outputs
+ * must not overlap inputs.  M == 0 writes zeros to dw_post and dw_pre.  The
+ * workspace works as in moe_align_ex; its size depends on (M, K) only.
+ *
+ * Errors: INVALID_ARG for null or misaligned pointers, negative sizes,
+ * eps <= 0, a bad h_dtype, or a combination other than those above;
+ * UNSUPPORTED for K >= 2^20, topk > 16 or M*topk >= 2^28; WORKSPACE.
+ */
+moe_status moe_block_norm(const void *h, const void *o, const float *gate, const float *w_post,
+                          const float *w_pre, int h_dtype, int M, int K, int topk, float res_scale,
+                          float eps, void *h_out, void *u, float *rstd_post, float *rstd_pre,
+                          void *stream);
+moe_status moe_block_norm_bwd(const void *dh_out, const void *du, const void *h_out, const void *o,
+                              const float *gate, const float *w_post, const float *w_pre,
+                              const float *rstd_post, const float *rstd_pre, int h_dtype, int M,
+                              int K, int topk, int du_topk, float res_scale, void *dh, void *d_o,
+                              float *dgate, float *dw_post, float *dw_pre, void *workspace,
+                              size_t *workspace_bytes, void *stream);
+
 /* Static, NUL-terminated name of a status code. */
 const char *moe_status_string(int status);
 

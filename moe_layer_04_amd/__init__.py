@@ -3,7 +3,7 @@
 The layer -- top-k softmax router, expert-sorted token permutation, grouped
 expert GEMMs with a fused SiLU*up epilogue, weighted un-permute combine --
 runs in hand-written HIP kernels behind the C ABI of include/moe.h
-(libmoe.so); this package is its thin ctypes binding plus the seeded input
+(libmoe.so), as one call or in pieces with their gradients; this package is its thin ctypes binding plus the seeded input
 generator used by tests and benchmarks.
 """
 from ._binding import (MOE_BF16, FusedForwardGraph, MOE_ERR_HIP, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
@@ -12,6 +12,8 @@ from ._binding import (MOE_BF16, FusedForwardGraph, MOE_ERR_HIP, MOE_ERR_INVALID
                        moe_align, moe_align_ex, moe_fused_forward, moe_fused_forward_noalloc,
                        moe_quant_rows_e4m3, moe_topk,
                        status_string, workspace_size)
+from ._operators import (moe_block_norm, moe_block_norm_bwd, moe_grouped_gemm, moe_grouped_gemm_dw,
+                         moe_grouped_gemm_dx, moe_silu_mul, moe_silu_mul_bwd)
 
 __all__ = [
     "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_ROWWISE", "MOE_MXFP4_E2M1", "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED",
@@ -20,4 +22,6 @@ __all__ = [
     "moe_quant_rows_e4m3", "moe_fused_forward", "status_string", "workspace_size",
     "FusedForwardGraph", "Plan", "fused_plan", "fused_routing", "moe_fused_forward_noalloc",
     "NOALLOC_SCRATCH_BYTES",
+    "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_silu_mul",
+    "moe_silu_mul_bwd", "moe_block_norm", "moe_block_norm_bwd",
 ]

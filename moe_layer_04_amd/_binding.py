@@ -37,7 +37,9 @@ MOE_REGIME_PREFILL = 2
 EXPORTS = ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3", "moe_fused_forward",
            "moe_fused_forward_ex", "moe_fused_forward_timed", "moe_fused_plan",
            "moe_fused_forward_noalloc", "moe_fused_graph_create", "moe_fused_graph_launch",
-           "moe_fused_graph_destroy", "moe_status_string")
+           "moe_fused_graph_destroy", "moe_grouped_gemm", "moe_grouped_gemm_dx",
+           "moe_grouped_gemm_dw", "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm",
+           "moe_block_norm_bwd", "moe_status_string")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -93,7 +95,18 @@ def load_library(build_if_missing: bool = False):
                                                ctypes.c_size_t, P, ctypes.POINTER(P)]
         lib.moe_fused_graph_launch.argtypes = [P, P]
         lib.moe_fused_graph_destroy.argtypes = [P]
+        F = ctypes.c_float
+        lib.moe_grouped_gemm.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P]
+        lib.moe_grouped_gemm_dx.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P]
+        lib.moe_grouped_gemm_dw.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, SZP, P]
+        lib.moe_silu_mul.argtypes = [P, P, P, P, I, I, I, P, P]
+        lib.moe_silu_mul_bwd.argtypes = [P, P, P, P, P, I, I, I, P, P, P]
+        lib.moe_block_norm.argtypes = [P, P, P, P, P, I, I, I, I, F, F, P, P, P, P, P]
+        lib.moe_block_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, F, P, P, P,
+                                           P, P, P, SZP, P]
         for name in ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3",
+                     "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
+                     "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm", "moe_block_norm_bwd",
                      "moe_fused_forward", "moe_fused_forward_ex", "moe_fused_forward_timed",
                      "moe_fused_plan", "moe_fused_forward_noalloc", "moe_fused_graph_create",
                      "moe_fused_graph_launch", "moe_fused_graph_destroy"):

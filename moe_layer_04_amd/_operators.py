@@ -1,0 +1,340 @@
+"""The layer in pieces, with gradients: matrix products grouped by expert, the
+gated activation between them and the norms around the block (the entry
+points of the same names in include/moe.h).
+
+As in the rest of the binding, tensors are dense and checked here, outputs
+and workspaces are torch allocations unless given, and the work runs on the
+current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from ._binding import MOE_ERR_WORKSPACE, MoEError, _check, load_library
+
+MOE_ROWS_GATHER = 1
+MOE_ROWS_SCATTER = 2
+MOE_ROWS_GATHER_DY = 4
+
+MOE_OUT_BF16 = 0
+MOE_OUT_FP32 = 1
+MOE_OUT_FP32_ADD = 2
+
+
+def _arg(t, name: str, dtype, shape, device):
+    """A dense GPU tensor of this dtype, shape (None: any extent) and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
+        raise ValueError(f"{name} must have shape {want}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device: torch.device, name: str, *args):
+    """One library call on the device's current stream, with that device
+    current."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, name)
+
+
+def _out(out, name: str, dtype, shape, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _arg(out, name, dtype, shape, device)
+
+
+def _workspace(device, workspace, nbytes: int):
+    """The caller's workspace, or one allocated here; the library checks the size."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _arg(workspace, "workspace", torch.uint8, (None,), device)
+    if workspace.numel() < nbytes:  # an empty one's null pointer would ask for the size
+        raise MoEError(MOE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, {nbytes} needed:")
+    return workspace
+
+
+def _rows(sorted_ids, expert_offsets, num_tokens, topk, gather_from, any_rows: bool, device):
+    """Checks the row arguments; returns (E, T).  gather_from: a gathered
+    operand (its rows are the tokens), or None."""
+    E = expert_offsets.shape[0] - 1 if expert_offsets.dim() == 1 else 0
+    _arg(expert_offsets, "expert_offsets", torch.int32, (None,), device)
+    if sorted_ids is None:
+        if any_rows:
+            raise ValueError("gather and scatter need sorted_ids")
+        return E, 0
+    _arg(sorted_ids, "sorted_ids", torch.int32, (None,), device)
+    if gather_from is not None:
+        if num_tokens is not None and num_tokens != gather_from.shape[0]:
+            raise ValueError(f"num_tokens is {num_tokens}, the gathered operand has "
+                             f"{gather_from.shape[0]} rows")
+        return E, gather_from.shape[0]
+    if num_tokens is None:
+        raise ValueError("num_tokens is needed with sorted_ids when nothing is gathered")
+    return E, int(num_tokens)
+
+
+def _product(name, rows_in, w, expert_offsets, sorted_ids, topk, num_tokens, gather, scatter, out,
+             dx: bool):
+    dev = w.device
+    _arg(w, "w", torch.bfloat16, (None, None, None), None)
+    E, N, K = w.shape
+    _arg(rows_in, "dy" if dx else "x", torch.bfloat16, (None, N if dx else K), dev)
+    En, T = _rows(sorted_ids, expert_offsets, num_tokens, topk, rows_in if gather else None,
+                  gather or scatter, dev)
+    if En != E:
+        raise ValueError(f"expert_offsets must have {E + 1} entries, got {En + 1}")
+    R = rows_in.shape[0] if sorted_ids is None else sorted_ids.shape[0]
+    if not gather and rows_in.shape[0] != R:
+        raise ValueError(f"the operand has {rows_in.shape[0]} rows, sorted_ids {R}")
+    out = _out(out, "out", torch.bfloat16, (T * topk if scatter else R, K if dx else N), dev)
+    rows = (MOE_ROWS_GATHER if gather else 0) | (MOE_ROWS_SCATTER if scatter else 0)
+    _call(dev, name, _p(rows_in), _p(w), _p(expert_offsets), _p(sorted_ids), rows, T, topk, R, E,
+          K, N, _p(out))
+    return out
+
+
+def moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor, *,
+                     sorted_ids: Optional[torch.Tensor] = None, topk: int = 1,
+                     num_tokens: Optional[int] = None, gather: bool = False,
+                     scatter: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[i] = w[e] x[i] for the sorted rows i of every expert e's range
+    (expert_offsets, sorted_ids: moe_align's).
+
+    x bf16 [R,K], or [num_tokens,K] with ``gather`` (row i reads the token of
+    its slot); w bf16 [E,N,K]; returns bf16 [R,N], or with ``scatter``
+    [num_tokens*topk,N] in slot order.  Rows of a new output that no sorted
+    row writes are uninitialised."""
+    return _product("moe_grouped_gemm", x, w, expert_offsets, sorted_ids, topk, num_tokens, gather,
+                    scatter, out, False)
+
+
+def moe_grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor, *,
+                        sorted_ids: Optional[torch.Tensor] = None, topk: int = 1,
+                        num_tokens: Optional[int] = None, gather: bool = False,
+                        scatter: bool = False,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx[i] = w[e]^T dy[i]: the gradient of moe_grouped_gemm's input rows.
+    dy bf16 [R,N] (or [num_tokens,N] with ``gather``); returns bf16 [R,K], or
+    [num_tokens*topk,K] with ``scatter``."""
+    return _product("moe_grouped_gemm_dx", dy, w, expert_offsets, sorted_ids, topk, num_tokens,
+                    gather, scatter, out, True)
+
+
+def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor, *,
+                        sorted_ids: Optional[torch.Tensor] = None, topk: int = 1,
+                        num_tokens: Optional[int] = None, gather_dy: bool = False,
+                        gather_x: bool = False, out_dtype: torch.dtype = torch.bfloat16,
+                        out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dw[e] = sum over e's rows of dy[i] x[i]^T, the gradient of
+    moe_grouped_gemm's weights: [E,N,K] in ``out_dtype`` (bf16 or fp32), or
+    into ``out``; ``accumulate`` adds to an fp32 ``out``.  gather_dy /
+    gather_x: that operand has num_tokens rows, read by the rows' tokens."""
+    dev = dy.device
+    _arg(dy, "dy", torch.bfloat16, (None, None), None)
+    _arg(x, "x", torch.bfloat16, (None, None), dev)
+    if gather_dy and gather_x and dy.shape[0] != x.shape[0]:
+        raise ValueError("two gathered operands must have the same number of rows")
+    E, T = _rows(sorted_ids, expert_offsets, num_tokens, topk,
+                 x if gather_x else dy if gather_dy else None, gather_dy or gather_x, dev)
+    N, K = dy.shape[1], x.shape[1]
+    R = dy.shape[0] if sorted_ids is None else sorted_ids.shape[0]
+    for t, name, gathered in ((dy, "dy", gather_dy), (x, "x", gather_x)):
+        if not gathered and t.shape[0] != R:
+            raise ValueError(f"{name} must have {R} rows, got {t.shape[0]}")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"the gradient must be bfloat16 or float32, got {out_dtype}")
+    if accumulate and (out is None or out_dtype != torch.float32):
+        raise ValueError("accumulate needs a float32 out")
+    out = _out(out, "out", out_dtype, (E, N, K), dev)
+    mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype == torch.float32 \
+        else MOE_OUT_BF16
+    rows = (MOE_ROWS_GATHER if gather_x else 0) | (MOE_ROWS_GATHER_DY if gather_dy else 0)
+    nbytes = ctypes.c_size_t(0)
+    sizes = (rows, T, topk, R, E, K, N, mode)
+    _check(load_library().moe_grouped_gemm_dw(None, None, None, None, *sizes, None, None,
+                                              ctypes.byref(nbytes), None),
+           "moe_grouped_gemm_dw (size query)")
+    workspace = _workspace(dev, workspace, nbytes.value)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    _call(dev, "moe_grouped_gemm_dw", _p(dy), _p(x), _p(expert_offsets), _p(sorted_ids), *sizes,
+          _p(out), _p(workspace), ctypes.byref(nbytes))
+    return out
+
+
+def _gated(g, topk_weights, sorted_ids, num_rows):
+    dev = g.device
+    _arg(g, "g", torch.bfloat16, (None, None), None)
+    R, two_n = g.shape
+    if two_n % 2:
+        raise ValueError("g must have an even number of columns (gate, up)")
+    slots = 0
+    if topk_weights is not None:
+        _arg(topk_weights, "topk_weights", torch.float32, (None,) * topk_weights.dim(), dev)
+        slots = topk_weights.numel()
+        if sorted_ids is None and slots != R:
+            raise ValueError(f"without sorted_ids topk_weights must have {R} values, got {slots}")
+    if sorted_ids is not None:
+        _arg(sorted_ids, "sorted_ids", torch.int32, (R,), dev)
+        if topk_weights is None:
+            raise ValueError("sorted_ids is for topk_weights")
+    if num_rows is not None:
+        _arg(num_rows, "num_rows", torch.int32, (1,), dev)
+    return dev, R, two_n // 2, slots
+
+
+def moe_silu_mul(g: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *,
+                 sorted_ids: Optional[torch.Tensor] = None,
+                 num_rows: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """a[i] = wt * silu(g[i,:N]) * g[i,N:], bf16 [R,N], with the routing
+    weight wt = topk_weights[sorted_ids[i]] (fp32, flat index; row i without
+    sorted_ids, 1 without weights).  Padding rows are zero; rows at and past
+    num_rows (moe_align's num_padded) are not written."""
+    dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
+    out = _out(out, "out", torch.bfloat16, (R, N), dev)
+    _call(dev, "moe_silu_mul", _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows), slots, R, N,
+          _p(out))
+    return out
+
+
+def moe_silu_mul_bwd(da: torch.Tensor, g: torch.Tensor,
+                     topk_weights: Optional[torch.Tensor] = None, *,
+                     sorted_ids: Optional[torch.Tensor] = None,
+                     num_rows: Optional[torch.Tensor] = None):
+    """Gradients of moe_silu_mul: (dg bf16 [R,2N], dtopk_weights in
+    topk_weights' shape, or None without weights).  Weights of slots that no
+    row names get an uninitialised gradient."""
+    dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
+    _arg(da, "da", torch.bfloat16, (R, N), dev)
+    dg = torch.empty_like(g)
+    dw = None if topk_weights is None else torch.empty_like(topk_weights)
+    _call(dev, "moe_silu_mul_bwd", _p(da), _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows),
+          slots, R, N, _p(dg), _p(dw))
+    return dg, dw
+
+
+def _stream_type(h, name: str) -> int:
+    if not isinstance(h, torch.Tensor) or h.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bfloat16 or float32 GPU tensor")
+    return MOE_OUT_FP32 if h.dtype == torch.float32 else MOE_OUT_BF16
+
+
+def moe_block_norm(h: torch.Tensor, o: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                   w_pre: Optional[torch.Tensor] = None, *, topk: int = 1, res_scale: float = 1.0,
+                   eps: float = 1e-6, out: Optional[torch.Tensor] = None):
+    """The norm after a block, its gate and residual scale, and the norm
+    before the next one:
+
+      h_out = h + res_scale * gate[t] * rmsnorm(sum_j o[t*topk + j]) * w_post
+      u     = rmsnorm(h_out) * w_pre
+
+    h bf16 or fp32 [M,K]; o bf16 [M*topk,K]; gate fp32 [M]; w_post, w_pre
+    fp32 [K].  Without o: only u, the norm of h.  Without w_post: the sum is
+    added without a norm.  Without w_pre: no u.  Returns (h_out, u, rstd_post,
+    rstd_pre), None where there is none; h_out is h without o.  ``out`` takes
+    h_out and may be h."""
+    kind = _stream_type(h, "h")
+    dev = h.device
+    M, K = _arg(h, "h", h.dtype, (None, None), None).shape
+    if w_pre is not None:
+        _arg(w_pre, "w_pre", torch.float32, (K,), dev)
+    if o is None:
+        if gate is not None or w_post is not None or out is not None:
+            raise ValueError("gate, w_post and out are for a block's output o")
+        if w_pre is None:
+            raise ValueError("one of o and w_pre is needed")
+    else:
+        _arg(o, "o", torch.bfloat16, (M * topk, K), dev)
+        if gate is not None:
+            _arg(gate, "gate", torch.float32, (M,), dev)
+        if w_post is not None:
+            _arg(w_post, "w_post", torch.float32, (K,), dev)
+        out = _out(out, "out", h.dtype, (M, K), dev)
+    u = None if w_pre is None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    r1 = None if w_post is None else torch.empty(M, dtype=torch.float32, device=dev)
+    r2 = None if w_pre is None else torch.empty(M, dtype=torch.float32, device=dev)
+    _call(dev, "moe_block_norm", _p(h), _p(o), _p(gate), _p(w_post), _p(w_pre), kind, M, K, topk,
+          res_scale, eps, _p(out), _p(u), _p(r1), _p(r2))
+    return (h if o is None else out), u, r1, r2
+
+
+def moe_block_norm_bwd(dh_out: Optional[torch.Tensor], du: Optional[torch.Tensor],
+                       h_out: torch.Tensor, o: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       w_post: Optional[torch.Tensor] = None,
+                       w_pre: Optional[torch.Tensor] = None,
+                       rstd_post: Optional[torch.Tensor] = None,
+                       rstd_pre: Optional[torch.Tensor] = None, *, topk: int = 1,
+                       du_topk: int = 1, res_scale: float = 1.0,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of moe_block_norm from those of h_out ([M,K] in its type, or
+    None) and of u (bf16 [M*du_topk,K], a token's rows are summed; None
+    without w_pre).  h_out, rstd_post and rstd_pre are the forward's.  Returns
+    (dh in h_out's type, do bf16 [M,K] -- the gradient of each of a token's
+    slots -- dgate fp32 [M], dw_post, dw_pre fp32 [K]), None where there is
+    none."""
+    kind = _stream_type(h_out, "h_out")
+    dev = h_out.device
+    M, K = _arg(h_out, "h_out", h_out.dtype, (None, None), None).shape
+    if dh_out is not None:
+        _arg(dh_out, "dh_out", h_out.dtype, (M, K), dev)
+    if (w_pre is None) != (du is None) or (w_pre is None) != (rstd_pre is None):
+        raise ValueError("du, w_pre and rstd_pre go together")
+    if (w_post is None) != (rstd_post is None):
+        raise ValueError("w_post and rstd_post go together")
+    if w_pre is not None:
+        _arg(w_pre, "w_pre", torch.float32, (K,), dev)
+        _arg(du, "du", torch.bfloat16, (M * du_topk, K), dev)
+        _arg(rstd_pre, "rstd_pre", torch.float32, (M,), dev)
+    elif dh_out is None or o is None:
+        raise ValueError("nothing to differentiate: give du, or dh_out and o")
+    if o is None:
+        if gate is not None or w_post is not None:
+            raise ValueError("gate and w_post are for a block's output o")
+    else:
+        _arg(o, "o", torch.bfloat16, (M * topk, K), dev)
+        if gate is not None:
+            _arg(gate, "gate", torch.float32, (M,), dev)
+        if w_post is not None:
+            _arg(w_post, "w_post", torch.float32, (K,), dev)
+            _arg(rstd_post, "rstd_post", torch.float32, (M,), dev)
+
+    def new(like, shape, dtype=torch.float32):
+        return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
+
+    dh = torch.empty_like(h_out)
+    do = new(o, (M, K), torch.bfloat16)
+    dgate, dw_post, dw_pre = new(gate, M), new(w_post, K), new(w_pre, K)
+    nbytes = ctypes.c_size_t(0)
+    _check(load_library().moe_block_norm_bwd(*[None] * 9, kind, M, K, topk, du_topk, res_scale,
+                                             *[None] * 6, ctypes.byref(nbytes), None),
+           "moe_block_norm_bwd (size query)")
+    workspace = _workspace(dev, workspace, nbytes.value)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    _call(dev, "moe_block_norm_bwd", _p(dh_out), _p(du), _p(h_out), _p(o), _p(gate), _p(w_post),
+          _p(w_pre), _p(rstd_post), _p(rstd_pre), kind, M, K, topk, du_topk, res_scale, _p(dh),
+          _p(do), _p(dgate), _p(dw_post), _p(dw_pre), _p(workspace), ctypes.byref(nbytes))
+    return dh, do, dgate, dw_post, dw_pre

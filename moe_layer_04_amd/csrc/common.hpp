@@ -124,6 +124,16 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return __longlong_as_double((long long)b0) + __longlong_as_double((long long)b1);
 }
 
+__device__ __forceinline__ float wave_sum_f32(float v) {
+    v += __uint_as_float(xchg_u32<0>(__float_as_uint(v)));
+    v += __uint_as_float(xchg_u32<1>(__float_as_uint(v)));
+    v += __uint_as_float(xchg_u32<2>(__float_as_uint(v)));
+    v += __uint_as_float(xchg_u32<3>(__float_as_uint(v)));
+    v += __uint_as_float(xchg_u32<4>(__float_as_uint(v)));
+    return __uint_as_float(readlane_u32(__float_as_uint(v), 0)) +
+           __uint_as_float(readlane_u32(__float_as_uint(v), 32));
+}
+
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // Max over all 64 lanes of a 64-bit key, result in every lane.

@@ -1,0 +1,86 @@
+// grouped.hpp -- what the kernels of the matrix products grouped by expert
+// share: their arguments, the row lookups and the search of a tile's expert.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+
+// moe_align's slot p = t*topk + j of sorted row i; anything outside
+// [0, slots) marks a padding row.  p / topk by a multiplication: with
+// magic = ceil(2^32 / topk) the product's upper half is exact for p*topk <
+// 2^32, that is for the fewer than 2^28 slots the entry points accept.
+// (topk == 1 has no 32-bit magic; its quotient is p.)
+__device__ __forceinline__ uint32_t grouped_token(uint32_t p, uint32_t magic) {
+    return magic ? __umulhi(p, magic) : p;
+}
+
+// Row of a gathered / scattered / plain operand for sorted row i, -1 for
+// padding.
+__device__ __forceinline__ int grouped_row(const GroupedArgs& g, int i, uint32_t how) {
+    if (!g.sorted) return i;
+    const uint32_t p = (uint32_t)g.sorted[i];
+    if (p >= g.slots) return -1;
+    if (how == kRowToken) return (int)grouped_token(p, g.magic);
+    return how == kRowSlot ? (int)p : i;
+}
+
+// Offsets are read clamped to [0, R], so that no list of offsets takes an
+// access out of the R rows.
+__device__ __forceinline__ int grouped_offset(const GroupedArgs& g, int e) {
+    return min(max(g.offsets[e], 0), g.R);
+}
+
+struct GroupedBlock {
+    int e;       // expert, -1: no such block
+    int row0;    // first sorted row of the block
+    int rows;    // rows of it (<= the block size)
+    int total;   // blocks of all experts
+};
+
+// Block `blk` of the list that gives every expert ceil(rows / B) blocks, in
+// expert order.  A wave holds four experts a lane and scans the block counts;
+// called by all 64 lanes of a wave, the result is wave-uniform.
+__device__ __forceinline__ GroupedBlock grouped_block(const GroupedArgs& g, int blk, int B) {
+    const int lane = lane_id();
+    int off[5], nb[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) off[j] = grouped_offset(g, min(4 * lane + j, g.E));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = max(off[j + 1] - off[j], 0);
+        nb[j] = (int)(((uint32_t)c + (uint32_t)B - 1) / (uint32_t)B);
+        sum += nb[j];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int v = __shfl_up(incl, d);
+        if (lane >= d) incl += v;
+    }
+    GroupedBlock r;
+    r.total = __builtin_amdgcn_readlane(incl, kWave - 1);
+    int start = incl - sum, e = -1, row0 = 0, rows = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (blk >= start && blk < start + nb[j]) {
+            e = 4 * lane + j;
+            row0 = off[j] + (blk - start) * B;
+            rows = min(off[j + 1] - row0, B);
+        }
+        start += nb[j];
+    }
+    const uint64_t hit = __ballot(e >= 0);
+    r.e = -1;
+    r.row0 = r.rows = 0;
+    if (hit) {
+        const int l = __builtin_ctzll(hit);
+        r.e = __builtin_amdgcn_readlane(e, l);
+        r.row0 = __builtin_amdgcn_readlane(row0, l);
+        r.rows = __builtin_amdgcn_readlane(rows, l);
+    }
+    return r;
+}
+
+}  // namespace moe

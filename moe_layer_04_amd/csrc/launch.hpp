@@ -162,4 +162,57 @@ void launch_decode_gemm2_combine_bf16(const void* act, const void* w2, const flo
                                       int M, int K, int N, int E, int topk, int cap, void* out,
                                       hipStream_t s);
 
+// ---- matrix products grouped by expert (grouped_gemm.hip) ---------------------
+// how an operand's rows are found from the sorted row i
+constexpr uint32_t kRowSorted = 0;  // row i
+constexpr uint32_t kRowToken = 1;   // row sorted[i] / topk
+constexpr uint32_t kRowSlot = 2;    // row sorted[i]
+struct GroupedArgs {
+    const uint16_t *w, *x, *dy;  // w [E,N,K]; x rows of K, dy rows of N (dw: no w; fwd: no dy; dx: no x)
+    const int32_t* offsets;      // [E+1], device
+    const int32_t* sorted;       // [R] slots, or null
+    uint32_t how_x, how_dy, how_out;
+    uint32_t slots, magic;       // slots = T*topk; magic of grouped_token
+    int T, R, E, K, N;
+    int out_f32, accumulate;
+    void* out;
+};
+void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);
+void launch_grouped_dx(const GroupedArgs& g, hipStream_t s);
+size_t grouped_dw_workspace(const GroupedArgs& g);
+void launch_grouped_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
+
+// ---- the gated activation between the products (gated_act.hip) ------------------
+struct GatedArgs {
+    const uint16_t *g, *da;   // g [R,2N] (gate, up), da [R,N]
+    const float* weights;     // per slot, or null
+    const int32_t* sorted;    // [R] slots, or null (slot i)
+    const int32_t* num_rows;  // device: rows at and past it stay as they are; or null
+    uint32_t slots;
+    int R, N;
+    uint16_t* out;            // forward: a [R,N]; backward: dg [R,2N]
+    float* dweights;          // per slot, or null
+};
+void launch_silu_mul(const GatedArgs& a, hipStream_t s);
+void launch_silu_mul_bwd(const GatedArgs& a, hipStream_t s);
+
+// ---- the norms around a block (block_norm.hip) -----------------------------------
+struct NormArgs {
+    const void* h;                         // forward: h; backward: h_out
+    const uint16_t *o, *du;                // o [M*topk,K]; du [M*du_topk,K]
+    const void* dh_out;
+    const float *gate, *w_post, *w_pre;
+    const float *rstd_post_in, *rstd_pre_in;  // backward
+    int M, K, topk, du_topk;
+    float res_scale, eps;
+    int h_f32;
+    void* h_out;                           // forward: h_out; backward: dh
+    uint16_t* u;                           // forward: u; backward: do
+    float *rstd_post, *rstd_pre;           // forward
+    float *dgate, *dw_post, *dw_pre;       // backward
+};
+void launch_block_norm(const NormArgs& a, hipStream_t s);
+size_t block_norm_bwd_workspace(int M, int K, bool post, bool pre);
+void launch_block_norm_bwd(const NormArgs& a, float* partials, hipStream_t s);
+
 }  // namespace moe
