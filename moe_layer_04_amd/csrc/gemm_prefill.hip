@@ -47,20 +47,13 @@
 // D[8*(v/4) + 4*(l/32) + v%4][l % 32], v = 0..15.
 #include "common.hpp"
 #include "launch.hpp"
+#include "tiles.hpp"
 #include "tuning.hpp"
 
 #include <type_traits>
 
 namespace moe {
 
-typedef __amdgpu_buffer_rsrc_t prsrc_t;
-
-__device__ __forceinline__ prsrc_t pmake_rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ f32x16_t mfma32_bf16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
 // e4m3 x e4m3, 64-deep; block scales fixed at 2^0 (E8M0 code 127)
 __device__ __forceinline__ f32x16_t mfma32_fp8(i32x8_t a, i32x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
@@ -105,44 +98,6 @@ struct TileWalk {
     }
 };
 
-// LDS rows: each operand row of a K-step is its BK elements (64 or 128
-// bytes) without padding, its 16-byte chunks permuted by an XOR of the row
-// index (swz, keyed by the chunks per row) so
-// that the 16 consecutive rows an MFMA operand read touches in one LDS cycle
-// land in distinct banks.  The DMA writes 1 KB per wave instruction in lane
-// order, so lane l of an instruction covering rows r0.. stores physical
-// chunk (l % CPR) of row r0 + l / CPR and therefore fetches logical chunk
-// (l % CPR) ^ swz(row) from global memory.
-template <int CPR>
-__device__ __forceinline__ int swz(int r) {
-    static_assert(CPR == 4 || CPR == 8, "64- or 128-byte LDS rows");
-    if constexpr (CPR == 4) return ((r >> 1) & 3) ^ ((r >> 3) & 1);
-    else return (r & 7) ^ ((r >> 3) & 1);
-}
-
-// s_waitcnt vmcnt(N) leaving the LDS/export counters unconstrained.
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// The wave's LDS accesses issued so far are complete (lgkmcnt(0)), and the
-// compiler moves no memory access across this point.  A wave's LDS
-// instructions execute in order, so after it the wave's lanes read what its
-// other lanes wrote before it.
-__device__ __forceinline__ void lds_wave_fence() {
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-}
-
-// v, computed where it is used: an epilogue address derived from it is not
-// hoisted to the kernel's start, where it would hold a register through the
-// main loop (the ping-pong loops use all 256)
-__device__ __forceinline__ int late_uniform(int v) {
-    __asm__ volatile("" : "+s"(v));
-    return v;
-}
-
 // Epilogue staging of fp32 results through a ping-pong wave's own LDS area
 // (kStagedRowsBytes: 64 token rows x 64 columns plus the rows' 64 slots).
 // Stored straight from the 32x32 accumulator layout, a store instruction
@@ -155,15 +110,6 @@ __device__ __forceinline__ int late_uniform(int v) {
 // >= nslots).
 constexpr int kStagedRowBytes = 64 * 4 + 16;  // the pad spreads a column's rows over the banks
 constexpr int kStagedRowsBytes = 64 * kStagedRowBytes + 64 * 4;
-
-// the lane's index, computed where it is used: per-lane epilogue addresses
-// are not hoisted to the kernel's start, where they would hold registers
-// through the main loop
-__device__ __forceinline__ int late_lane() {
-    int v;
-    __asm__ volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(v));
-    return v;
-}
 
 // lane: late_lane() of the epilogue
 __device__ __forceinline__ void stage_put(char* st, int lane, int b, int a, int vg, f32x4_t v) {

@@ -36,22 +36,28 @@ struct GroupedBlock {
     int e;       // expert, -1: no such block
     int row0;    // first sorted row of the block
     int rows;    // rows of it (<= the block size)
-    int total;   // blocks of all experts
 };
 
-// Block `blk` of the list that gives every expert ceil(rows / B) blocks, in
-// expert order.  A wave holds four experts a lane and scans the block counts;
-// called by all 64 lanes of a wave, the result is wave-uniform.
-__device__ __forceinline__ GroupedBlock grouped_block(const GroupedArgs& g, int blk, int B) {
+// The list that gives every expert ceil(rows / B) blocks, in expert order,
+// spread over a wave: a lane holds four experts' offsets and block counts.
+struct GroupedScan {
+    int off[5], nb[4];
+    int start;   // the lane's first block
+    int total;   // blocks of all experts (wave-uniform)
+};
+
+// called by all 64 lanes of a wave
+__device__ __forceinline__ GroupedScan grouped_scan(const GroupedArgs& g, int B) {
     const int lane = lane_id();
-    int off[5], nb[4], sum = 0;
+    GroupedScan s;
+    int sum = 0;
 #pragma unroll
-    for (int j = 0; j < 5; ++j) off[j] = grouped_offset(g, min(4 * lane + j, g.E));
+    for (int j = 0; j < 5; ++j) s.off[j] = grouped_offset(g, min(4 * lane + j, g.E));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int c = max(off[j + 1] - off[j], 0);
-        nb[j] = (int)(((uint32_t)c + (uint32_t)B - 1) / (uint32_t)B);
-        sum += nb[j];
+        const int c = max(s.off[j + 1] - s.off[j], 0);
+        s.nb[j] = (int)(((uint32_t)c + (uint32_t)B - 1) / (uint32_t)B);
+        sum += s.nb[j];
     }
     int incl = sum;
 #pragma unroll
@@ -59,21 +65,26 @@ __device__ __forceinline__ GroupedBlock grouped_block(const GroupedArgs& g, int 
         const int v = __shfl_up(incl, d);
         if (lane >= d) incl += v;
     }
-    GroupedBlock r;
-    r.total = __builtin_amdgcn_readlane(incl, kWave - 1);
-    int start = incl - sum, e = -1, row0 = 0, rows = 0;
+    // ascending offsets never reach the bound, which the launch grids cover
+    s.total = min(__builtin_amdgcn_readlane(incl, kWave - 1), g.R / B + min(g.R, g.E));
+    s.start = incl - sum;
+    return s;
+}
+
+// block `blk` of the list (wave-uniform, as is the result)
+__device__ __forceinline__ GroupedBlock grouped_find(const GroupedScan& s, int blk, int B) {
+    int start = s.start, e = -1, row0 = 0, rows = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (blk >= start && blk < start + nb[j]) {
-            e = 4 * lane + j;
-            row0 = off[j] + (blk - start) * B;
-            rows = min(off[j + 1] - row0, B);
+        if (blk >= start && blk < start + s.nb[j]) {
+            e = 4 * lane_id() + j;
+            row0 = s.off[j] + (blk - start) * B;
+            rows = min(s.off[j + 1] - row0, B);
         }
-        start += nb[j];
+        start += s.nb[j];
     }
+    GroupedBlock r = {-1, 0, 0};
     const uint64_t hit = __ballot(e >= 0);
-    r.e = -1;
-    r.row0 = r.rows = 0;
     if (hit) {
         const int l = __builtin_ctzll(hit);
         r.e = __builtin_amdgcn_readlane(e, l);

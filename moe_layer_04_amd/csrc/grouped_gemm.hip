@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256, 4) void grouped_any_kernel(GroupedArgs g) {
         rows = max(grouped_offset(g, e + 1) - row0, 0);
         red = rows;
     } else {
-        const GroupedBlock b = grouped_block(g, bt, kSimTile);
+        const GroupedBlock b = grouped_find(grouped_scan(g, kSimTile), bt, kSimTile);
         if (b.e < 0) return;
         e = b.e;
         row0 = b.row0;
@@ -153,9 +153,21 @@ void launch_any(const GroupedArgs& g, hipStream_t s) {
 
 }  // namespace
 
-void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) { launch_any<kOpFwd>(g, s); }
-void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) { launch_any<kOpDx>(g, s); }
+// full tiles: every row of an operand is whole 16-byte chunks
+static bool tiles_fit(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
+
+void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
+    if (tiles_fit(g)) launch_grouped_tiles_fwd(g, s);
+    else launch_any<kOpFwd>(g, s);
+}
+void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {
+    if (tiles_fit(g)) launch_grouped_tiles_dx(g, s);
+    else launch_any<kOpDx>(g, s);
+}
 size_t grouped_dw_workspace(const GroupedArgs&) { return 0; }
-void launch_grouped_dw(const GroupedArgs& g, void*, hipStream_t s) { launch_any<kOpDw>(g, s); }
+void launch_grouped_dw(const GroupedArgs& g, void*, hipStream_t s) {
+    if (tiles_fit(g)) launch_grouped_tiles_dw(g, s);
+    else launch_any<kOpDw>(g, s);
+}
 
 }  // namespace moe

@@ -179,6 +179,10 @@ struct GroupedArgs {
 };
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);
 void launch_grouped_dx(const GroupedArgs& g, hipStream_t s);
+// full 256 x 256 tiles (K and N multiples of 8)
+void launch_grouped_tiles_fwd(const GroupedArgs& g, hipStream_t s);
+void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s);
+void launch_grouped_tiles_dw(const GroupedArgs& g, hipStream_t s);
 size_t grouped_dw_workspace(const GroupedArgs& g);
 void launch_grouped_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
 
