@@ -13,7 +13,7 @@ namespace moe {
 // 2^32, that is for the fewer than 2^28 slots the entry points accept.
 // (topk == 1 has no 32-bit magic; its quotient is p.)
 __device__ __forceinline__ uint32_t grouped_token(uint32_t p, uint32_t magic) {
-    return magic ? __umulhi(p, magic) : p;
+    return __umulhi(p, magic) + (magic ? 0u : p);
 }
 
 // Row of a gathered / scattered / plain operand for sorted row i, -1 for

@@ -42,107 +42,93 @@ constexpr int kInstr = kSlotBytes / 1024 / 4;         // copies of a wave per st
 // output tiles of one A column group that consecutive tiles share (see tile order below)
 constexpr int kGroup = 4;
 
-// Where a tile's operand comes from.
-struct Source {
-    const char* base;   // row: first row of the tile; column: row 0 of the reduction, tile's column
-    uint32_t bytes;     // row: covered from base; column, token rows: likewise
-    uint32_t ld;        // bytes per row
-    int red;            // reduction elements
-    int col0;           // column: byte offset of the tile's first column within a row
-};
+// Copies of an operand's step.  A wave copies one operand, 1 KB an instruction
+// and kInstr of them a step; off[q] is the lane's source offset of copy q,
+// held once for either kind of operand.
+typedef uint32_t Offsets[kInstr];
 
-template <bool LOOK>
+// "Row" operand: 256 rows of 64 reduction elements from a descriptor that
+// covers the tile's rows (or, for gathered rows, the whole operand).
 struct RowCopy {
+    static constexpr bool kLook = false;  // its lookups are done once, before the loop
     prsrc_t r;
-    uint32_t ld, red_bytes, lane_off, chunk;
-    uint32_t off[LOOK ? kInstr : 1];
+    uint32_t red_bytes;
 
-    // rows: row of lane's copy q in the operand (LOOK), -1 padding; else the tile's rows in order
-    __device__ __forceinline__ void init(const Source& s, int gw, int lane) {
-        r = pmake_rsrc(s.base, s.bytes);
-        ld = s.ld;
-        red_bytes = (uint32_t)s.red * 2;
-        // row (q*4 + gw)*8 + lane/8: its swizzle is the same for every q
-        chunk = (uint32_t)(((lane & 7) ^ swz<8>(gw * 8 + lane / 8)) << 4);
-        lane_off = (uint32_t)(gw * 8 + lane / 8) * ld + chunk;
-    }
+    // row of the tile that the lane's copy q fills, and its chunk of the
+    // row: physical chunk lane % 8; the swizzle is the same for every q
     __device__ static __forceinline__ int row(int q, int gw, int lane) {
         return (q * 4 + gw) * 8 + lane / 8;
     }
-    __device__ __forceinline__ void copy(char* slot, int step, int gw) const {
+    __device__ static __forceinline__ uint32_t chunk(int gw, int lane) {
+        return (uint32_t)(((lane & 7) ^ swz<8>(gw * 8 + lane / 8)) << 4);
+    }
+    __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
         typedef __attribute__((address_space(3))) void* lds_ptr_t;
         const uint32_t kb = (uint32_t)step * (kStep * 2);
-        const bool out = kb + chunk >= red_bytes;  // false for every lane before the last step
+        // the last step of a reduction that is no multiple of 64
+        const bool cut = kb + kStep * 2 > red_bytes && kb + chunk(gw, late_lane()) >= red_bytes;
 #pragma unroll
-        for (int q = 0; q < kInstr; ++q) {
-            uint32_t v = LOOK ? off[q] : lane_off + (uint32_t)(q * 32) * ld;
-            v = out ? kNowhere : v + kb;
+        for (int q = 0; q < kInstr; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(slot + (q * 4 + gw) * 1024), 16,
-                                                     v, 0, 0, 0);
-        }
+                                                     cut ? kNowhere : off[q] + kb, 0, 0, 0);
     }
 };
 
+// "Column" operand: 64 rows of 256 columns.  LOOK: a row is found by its slot
+// -- the slot's token (`token`, rows anywhere in the operand), or its position,
+// with padding rows as zeros; else rows in order.
 template <bool LOOK>
 struct ColCopy {
-    // LOOK: the expert's slots, through the scalar loads of the constant address
-    // space (no kernel writes them; vector loads would count with the copies)
-    typedef const __attribute__((address_space(4))) int32_t* ids_t;
-    const char* base;
-    ids_t ids;
-    uint32_t ld, bytes, lane_off, chunk, slots, magic;
-    int red, col0, half;
-    bool token;           // LOOK: rows by token (fixed base) or by position
-    int next[LOOK ? 2 * kInstr : 1];
+    static constexpr bool kLook = LOOK;
+    const char* base;     // the tile's first column in the expert's first row (token: in row 0)
+    const int32_t* ids;   // LOOK: the expert's slots
+    uint32_t ld, bytes;   // bytes a row; token: bytes that base covers
+    uint32_t col0;        // bytes before the tile's first column in a row
+    uint32_t slots, magic;
+    int red;              // rows
+    bool token;
 
-    __device__ __forceinline__ void init(const Source& s, int gw, int lane) {
-        base = s.base;
-        bytes = s.bytes;
-        ld = s.ld;
-        red = s.red;
-        col0 = s.col0;
-        half = lane >> 5;
-        // row 2*(q*4 + gw) + lane/32 of the step; its low three bits are the same for every q
-        const int x = (2 * gw + half) & 7;
-        chunk = (uint32_t)(((((lane & 31) >> 2) ^ x) * 4 + (lane & 3)) << 4);
-        lane_off = (uint32_t)(2 * gw + half) * ld + chunk;
+    // row 2*(q*4 + gw) + lane/32 of a step: its low three bits, the same for
+    // every q, and the lane's chunk of it
+    __device__ static __forceinline__ int low(int gw, int lane) { return 2 * gw + (lane >> 5); }
+    __device__ static __forceinline__ uint32_t chunk(int gw, int lane) {
+        return (uint32_t)(((((lane & 31) >> 2) ^ low(gw, lane)) * 4 + (lane & 3)) << 4);
     }
-    // the slots of the rows this wave copies at `step` (wave-uniform loads)
-    __device__ __forceinline__ void look(int step, int gw) {
-        if constexpr (LOOK) {
-            const int last = red - 1;
+    __device__ __forceinline__ void in_order(Offsets& off, int gw, int lane) const {
 #pragma unroll
-            for (int q = 0; q < kInstr; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = step * kStep + 2 * (q * 4 + gw) + h;
-                    next[2 * q + h] = last < 0 ? -1 : ids[min(i, last)];
-                }
-        }
+        for (int q = 0; q < kInstr; ++q)
+            off[q] = (uint32_t)(q * 8 + low(gw, lane)) * ld + chunk(gw, lane);
     }
-    __device__ __forceinline__ void copy(char* slot, int step, int gw) const {
+    // Looking rows up takes three steps, so that none waits for memory: fetch
+    // loads the slot of row `lane` of a step (one load a wave, a step before
+    // its copy is placed), place turns it into the row's offset and hands each
+    // lane those of the rows it copies, copy issues the copies.
+    __device__ __forceinline__ int fetch(int step, int lane) const {
+        return red > 0 ? ids[min(step * kStep + lane, red - 1)] : -1;
+    }
+    __device__ __forceinline__ void place(Offsets& off, int id, int step, int gw, int lane) const {
+        const uint32_t p = (uint32_t)id;
+        const uint32_t row = token ? grouped_token(p, magic) : (uint32_t)lane;
+        const bool ok = (p < slots) & (step * kStep + lane < red);
+        const uint32_t at = ok ? row * ld : kNowhere;
+#pragma unroll
+        for (int q = 0; q < kInstr; ++q)
+            off[q] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * low(gw, lane) + 32 * q, (int)at) +
+                     chunk(gw, lane);
+    }
+    __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
         typedef __attribute__((address_space(3))) void* lds_ptr_t;
-        const int row0 = step * kStep;
         const bool fixed = LOOK && token;
+        const int row0 = step * kStep;
         // the descriptor starts at the step's first row, so that offsets stay
-        // small however many rows the expert has
+        // small however many rows there are
         const uint32_t rows = (uint32_t)min(red - row0, kStep);
         const prsrc_t r = pmake_rsrc(base + (fixed ? 0 : (size_t)row0 * ld),
-                                     fixed ? bytes : rows * ld - (uint32_t)col0);
+                                     fixed ? bytes : rows * ld - col0);
 #pragma unroll
-        for (int q = 0; q < kInstr; ++q) {
-            uint32_t v;
-            if constexpr (LOOK) {
-                const int i = 2 * (q * 4 + gw) + half;
-                const uint32_t p = (uint32_t)(half ? next[2 * q + 1] : next[2 * q]);
-                const uint32_t row = token ? grouped_token(p, magic) : (uint32_t)i;
-                v = p < slots && row0 + i < red ? row * ld + chunk : kNowhere;
-            } else {
-                v = lane_off + (uint32_t)(q * 8) * ld;
-            }
+        for (int q = 0; q < kInstr; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(slot + (q * 4 + gw) * 1024), 16,
-                                                     v, 0, 0, 0);
-        }
+                                                     off[q], 0, 0, 0);
     }
 };
 
@@ -195,8 +181,8 @@ struct PingPong {
     }
 
     template <bool COMPUTE>
-    __device__ __forceinline__ void run(char* lds, CopyA& ca, CopyB& cb, int steps, int wave,
-                                        int arow0, int brow0) {
+    __device__ __forceinline__ void run(char* lds, const CopyA& ca, const CopyB& cb, Offsets& off,
+                                        int steps, int wave, int arow0, int brow0) {
         const int lane = lane_id();
         const bool second = wave >= 4;  // wave-uniform
         const int gw = wave & 3;
@@ -219,19 +205,31 @@ struct PingPong {
         rb.init(brow0, lane);
         bf16x8_t fa[4][4], fb[4][2];
 
+        int id = -1;  // slot of the step after the next copy
         barrier();
         if (!second) {
-            if constexpr (BCOL) cb.look(0, gw);
-            if (steps > 0) cb.copy(slot_b(0), 0, gw);
-            if constexpr (BCOL) cb.look(1, gw);
+            int id0 = -1;
+            if constexpr (CopyB::kLook) {
+                id0 = cb.fetch(0, lane);
+                id = cb.fetch(1, lane);
+                cb.place(off, id0, 0, gw, lane);
+            }
+            if (steps > 0) cb.copy(off, slot_b(0), 0, gw);
+            if constexpr (CopyB::kLook) cb.place(off, id, 1, gw, lane);
             wait_vmcnt<0>();
         } else {
-            if constexpr (ACOL) ca.look(0, gw);
-            if (steps > 0) ca.copy(slot_a(0), 0, gw);
-            if constexpr (ACOL) ca.look(1, gw);
+            int id0 = -1, id1 = -1;
+            if constexpr (CopyA::kLook) {
+                id0 = ca.fetch(0, lane);
+                id1 = ca.fetch(1, lane);
+                id = ca.fetch(2, lane);
+                ca.place(off, id0, 0, gw, lane);
+            }
+            if (steps > 0) ca.copy(off, slot_a(0), 0, gw);
             if (steps > 1) {
-                ca.copy(slot_a(1), 1, gw);
-                if constexpr (ACOL) ca.look(2, gw);
+                if constexpr (CopyA::kLook) ca.place(off, id1, 1, gw, lane);
+                ca.copy(off, slot_a(1), 1, gw);
+                if constexpr (CopyA::kLook) ca.place(off, id, 2, gw, lane);
                 wait_vmcnt<kInstr>();
             } else {
                 wait_vmcnt<0>();
@@ -253,13 +251,13 @@ struct PingPong {
             }
             if (!second) {
                 if (s + 1 < steps) {
-                    cb.copy(slot_b(bsl ^ 1), s + 1, gw);
-                    if constexpr (BCOL) cb.look(s + 2, gw);
+                    if constexpr (CopyB::kLook) id = cb.fetch(s + 2, lane);
+                    cb.copy(off, slot_b(bsl ^ 1), s + 1, gw);
                 }
             } else {
                 if (s + 2 < steps) {
-                    ca.copy(slot_a(asl == 0 ? 2 : asl - 1), s + 2, gw);
-                    if constexpr (ACOL) ca.look(s + 3, gw);
+                    if constexpr (CopyA::kLook) id = ca.fetch(s + 3, lane);
+                    ca.copy(off, slot_a(asl == 0 ? 2 : asl - 1), s + 2, gw);
                     wait_vmcnt<kInstr>();
                 } else {
                     wait_vmcnt<0>();
@@ -277,7 +275,12 @@ struct PingPong {
                         for (int b = 0; b < 2; ++b)
                             acc[a][b] = mfma32_bf16(fa[ks][a], fb[ks][b], acc[a][b]);
             }
-            if (!second) wait_vmcnt<0>();
+            if (!second) {
+                if constexpr (CopyB::kLook) cb.place(off, id, s + 2, gw, lane);
+                wait_vmcnt<0>();
+            } else if constexpr (CopyA::kLook) {
+                ca.place(off, id, s + 3, gw, lane);
+            }
             barrier();
             asl = asl + 1 == kASlots ? 0 : asl + 1;
             bsl ^= 1;
@@ -391,38 +394,51 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     const uint16_t* src = DX ? g.dy : g.x;
     const uint32_t how = DX ? g.how_dy : g.how_x;
     const uint32_t ld_b = (uint32_t)red * 2;
-    typedef typename std::conditional<DX, ColCopy<false>, RowCopy<false>>::type CopyA;
-    typedef RowCopy<LOOK> CopyB;
+    typedef typename std::conditional<DX, ColCopy<false>, RowCopy>::type CopyA;
     CopyA ca;
-    CopyB cb;
-    if constexpr (DX)
-        ca.init(Source{(const char*)(w + a0), 0, (uint32_t)g.K * 2, red, a0 * 2}, gw, lane);
-    else
-        ca.init(Source{(const char*)(w + (size_t)a0 * g.K),
-                       (uint32_t)min(cols - a0, kTile) * (uint32_t)(g.K * 2), (uint32_t)g.K * 2, red,
-                       0}, gw, lane);
+    RowCopy cb;
+    Offsets off;
+    if constexpr (DX) {
+        ca.base = (const char*)(w + a0);
+        ca.ld = (uint32_t)g.K * 2;
+        ca.col0 = (uint32_t)a0 * 2;
+        ca.red = red;
+    } else {
+        ca.r = pmake_rsrc(w + (size_t)a0 * g.K, (uint32_t)min(cols - a0, kTile) * ld_b);
+        ca.red_bytes = ld_b;
+    }
     const bool by_token = LOOK && how == kRowToken;
-    cb.init(Source{(const char*)(by_token ? src : src + (size_t)blk.row0 * red),
-                   (uint32_t)(by_token ? g.T : blk.rows) * ld_b, ld_b, red, 0}, gw, lane);
-    if constexpr (LOOK) {
+    cb.r = pmake_rsrc(by_token ? src : src + (size_t)blk.row0 * red,
+                      (uint32_t)(by_token ? g.T : blk.rows) * ld_b);
+    cb.red_bytes = ld_b;
+    if (DX && wave >= 4) {
+        if constexpr (DX) ca.in_order(off, gw, lane);
+    } else {
+        const uint32_t chunk = RowCopy::chunk(gw, lane);
         uint32_t p[kInstr];
+        if constexpr (LOOK) {
 #pragma unroll
-        for (int q = 0; q < kInstr; ++q)  // in flight together
-            p[q] = (uint32_t)g.sorted[blk.row0 + min(CopyB::row(q, gw, lane), blk.rows - 1)];
+            for (int q = 0; q < kInstr; ++q)  // in flight together
+                p[q] = (uint32_t)g.sorted[blk.row0 + min(RowCopy::row(q, gw, lane), blk.rows - 1)];
+        }
 #pragma unroll
         for (int q = 0; q < kInstr; ++q) {
-            const int j = CopyB::row(q, gw, lane);
-            const uint32_t row = by_token ? grouped_token(p[q], g.magic) : (uint32_t)j;
-            cb.off[q] = j < blk.rows && p[q] < g.slots ? row * ld_b + cb.chunk : kNowhere;
+            uint32_t j = (uint32_t)RowCopy::row(q, gw, lane);
+            bool ok = true;  // past the tile's rows the descriptor ends
+            if (LOOK && wave < 4) {
+                ok = (j < (uint32_t)blk.rows) & (p[q] < g.slots);
+                if (by_token) j = grouped_token(p[q], g.magic);
+            }
+            off[q] = ok ? j * ld_b + chunk : kNowhere;
         }
     }
     // wave tile: 128 columns x 64 rows, 2 x 2 waves in each half of the rows
     const int arow0 = (gw & 1) * 128, brow0 = (wave >> 2) * 128 + (gw >> 1) * 64;
     const bool used = brow0 < blk.rows;
     const int steps = (red + kStep - 1) / kStep;
-    PingPong<DX, false, CopyA, CopyB> core;
-    if (used) core.template run<true>(lds, ca, cb, steps, wave, arow0, brow0);
-    else core.template run<false>(lds, ca, cb, steps, wave, arow0, brow0);
+    PingPong<DX, false, CopyA, RowCopy> core;
+    if (used) core.template run<true>(lds, ca, cb, off, steps, wave, arow0, brow0);
+    else core.template run<false>(lds, ca, cb, off, steps, wave, arow0, brow0);
     if (used) {
         const int j = brow0 + late_lane();
         long row = -1;
@@ -459,27 +475,29 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
     const int rows = max(__builtin_amdgcn_readfirstlane(grouped_offset(g, e + 1)) - row0, 0);
     if (rows == 0 && g.accumulate) return;
 
-    typedef ColCopy<LOOK> Copy;
-    auto source = [&](Copy& c, const uint16_t* p, int width, int first, uint32_t how) {
-        const bool token = LOOK && how == kRowToken;
-        const uint32_t ld = (uint32_t)width * 2;
-        c.init(Source{(const char*)(p + (token ? 0 : (size_t)row0 * width) + first),
-                      g.T > 0 ? (uint32_t)g.T * ld - (uint32_t)first * 2 : 0, ld, rows, first * 2},
-               gw, lane);
-        c.ids = (typename Copy::ids_t)(g.sorted + row0);
-        c.slots = g.slots;
-        c.magic = g.magic;
-        c.token = token;
-    };
-    Copy ca, cb;
-    source(ca, g.x, g.K, a0, g.how_x);
-    source(cb, g.dy, g.N, b0, g.how_dy);
+    // a wave copies one operand: waves 4-7 x (A), waves 0-3 dy (B)
+    const bool is_x = wave >= 4;
+    const uint16_t* p = is_x ? g.x : g.dy;
+    const int width = is_x ? g.K : g.N, first = is_x ? a0 : b0;
+    const uint32_t ld = (uint32_t)width * 2;
+    ColCopy<LOOK> copy;
+    copy.token = LOOK && (is_x ? g.how_x : g.how_dy) == kRowToken;
+    copy.base = (const char*)(p + (copy.token ? 0 : (size_t)row0 * width) + first);
+    copy.ld = ld;
+    copy.col0 = (uint32_t)first * 2;
+    copy.bytes = g.T > 0 ? (uint32_t)g.T * ld - copy.col0 : 0;
+    copy.red = rows;
+    copy.ids = g.sorted + row0;
+    copy.slots = g.slots;
+    copy.magic = g.magic;
+    Offsets off;
+    if constexpr (!LOOK) copy.in_order(off, gw, lane);
     const int arow0 = (gw & 1) * 128, brow0 = (wave >> 2) * 128 + (gw >> 1) * 64;
     const bool used = b0 + brow0 < g.N && a0 + arow0 < g.K;
     const int steps = (rows + kStep - 1) / kStep;
-    PingPong<true, true, Copy, Copy> core;
-    if (used) core.template run<true>(lds, ca, cb, steps, wave, arow0, brow0);
-    else core.template run<false>(lds, ca, cb, steps, wave, arow0, brow0);
+    PingPong<true, true, ColCopy<LOOK>, ColCopy<LOOK>> core;
+    if (used) core.template run<true>(lds, copy, copy, off, steps, wave, arow0, brow0);
+    else core.template run<false>(lds, copy, copy, off, steps, wave, arow0, brow0);
     if (used) {
         const int n = b0 + brow0 + late_lane();
         store_tile(lds + gw * kStArea, core.acc, n < g.N ? ((long)e * g.N + n) * g.K : -1, a0 + arow0,
