@@ -32,6 +32,14 @@ __device__ __forceinline__ int grouped_offset(const GroupedArgs& g, int e) {
     return min(max(g.offsets[e], 0), g.R);
 }
 
+// the same of a wave-uniform expert, by a scalar load (no kernel writes the
+// offsets): it neither waits for nor counts with the vector loads and stores
+// in flight
+__device__ __forceinline__ int grouped_offset_scalar(const GroupedArgs& g, int e) {
+    typedef const __attribute__((address_space(4))) int32_t* scalar_t;
+    return min(max(((scalar_t)g.offsets)[e], 0), g.R);
+}
+
 struct GroupedBlock {
     int e;       // expert, -1: no such block
     int row0;    // first sorted row of the block

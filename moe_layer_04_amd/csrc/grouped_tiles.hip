@@ -41,6 +41,7 @@ constexpr int kLds = (kASlots + kBSlots) * kSlotBytes;
 constexpr int kInstr = kSlotBytes / 1024 / 4;         // copies of a wave per step
 // output tiles of one A column group that consecutive tiles share (see tile order below)
 constexpr int kGroup = 4;
+constexpr int kCusPerXcd = 32;
 
 // Copies of an operand's step.  A wave copies one operand, 1 KB an instruction
 // and kInstr of them a step; off[q] is the lane's source offset of copy q,
@@ -50,7 +51,6 @@ typedef uint32_t Offsets[kInstr];
 // "Row" operand: 256 rows of 64 reduction elements from a descriptor that
 // covers the tile's rows (or, for gathered rows, the whole operand).
 struct RowCopy {
-    static constexpr bool kLook = false;  // its lookups are done once, before the loop
     prsrc_t r;
     uint32_t red_bytes;
 
@@ -74,61 +74,40 @@ struct RowCopy {
     }
 };
 
-// "Column" operand: 64 rows of 256 columns.  LOOK: a row is found by its slot
-// -- the slot's token (`token`, rows anywhere in the operand), or its position,
-// with padding rows as zeros; else rows in order.
-template <bool LOOK>
+// "Column" operand: 64 rows of 256 columns, 16 consecutive rows a wave, two an
+// instruction.  Row 16*gw + 2*q + lane/32 has its 64-byte pieces permuted by
+// its low three bits, 2*(q%4) + lane/32.
 struct ColCopy {
-    static constexpr bool kLook = LOOK;
-    const char* base;     // the tile's first column in the expert's first row (token: in row 0)
-    const int32_t* ids;   // LOOK: the expert's slots
-    uint32_t ld, bytes;   // bytes a row; token: bytes that base covers
+    const char* base;     // the tile's first column in row 0
+    uint32_t ld;          // bytes a row
     uint32_t col0;        // bytes before the tile's first column in a row
-    uint32_t slots, magic;
     int red;              // rows
-    bool token;
 
-    // row 2*(q*4 + gw) + lane/32 of a step: its low three bits, the same for
-    // every q, and the lane's chunk of it
-    __device__ static __forceinline__ int low(int gw, int lane) { return 2 * gw + (lane >> 5); }
-    __device__ static __forceinline__ uint32_t chunk(int gw, int lane) {
-        return (uint32_t)(((((lane & 31) >> 2) ^ low(gw, lane)) * 4 + (lane & 3)) << 4);
+    // the lane's chunk of its row at copy q
+    __device__ static __forceinline__ uint32_t chunk(int q, int lane) {
+        return ((uint32_t)((((lane & 31) >> 2) ^ (lane >> 5)) << 6) | (uint32_t)((lane & 3) << 4)) ^
+               (uint32_t)((q & 3) << 7);
     }
-    __device__ __forceinline__ void in_order(Offsets& off, int gw, int lane) const {
+    // offsets of rows in order, from a step's first row
+    __device__ static __forceinline__ void in_order(Offsets& off, uint32_t ld, int gw, int lane) {
 #pragma unroll
         for (int q = 0; q < kInstr; ++q)
-            off[q] = (uint32_t)(q * 8 + low(gw, lane)) * ld + chunk(gw, lane);
+            off[q] = (uint32_t)(gw * 16 + 2 * q + (lane >> 5)) * ld + chunk(q, lane);
     }
-    // Looking rows up takes three steps, so that none waits for memory: fetch
-    // loads the slot of row `lane` of a step (one load a wave, a step before
-    // its copy is placed), place turns it into the row's offset and hands each
-    // lane those of the rows it copies, copy issues the copies.
-    __device__ __forceinline__ int fetch(int step, int lane) const {
-        return red > 0 ? ids[min(step * kStep + lane, red - 1)] : -1;
-    }
-    __device__ __forceinline__ void place(Offsets& off, int id, int step, int gw, int lane) const {
-        const uint32_t p = (uint32_t)id;
-        const uint32_t row = token ? grouped_token(p, magic) : (uint32_t)lane;
-        const bool ok = (p < slots) & (step * kStep + lane < red);
-        const uint32_t at = ok ? row * ld : kNowhere;
-#pragma unroll
-        for (int q = 0; q < kInstr; ++q)
-            off[q] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * low(gw, lane) + 32 * q, (int)at) +
-                     chunk(gw, lane);
-    }
-    __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
+    __device__ static __forceinline__ void issue(const prsrc_t r, const Offsets& off, char* slot,
+                                                 int gw) {
         typedef __attribute__((address_space(3))) void* lds_ptr_t;
-        const bool fixed = LOOK && token;
-        const int row0 = step * kStep;
-        // the descriptor starts at the step's first row, so that offsets stay
-        // small however many rows there are
-        const uint32_t rows = (uint32_t)min(red - row0, kStep);
-        const prsrc_t r = pmake_rsrc(base + (fixed ? 0 : (size_t)row0 * ld),
-                                     fixed ? bytes : rows * ld - col0);
 #pragma unroll
         for (int q = 0; q < kInstr; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(slot + (q * 4 + gw) * 1024), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(slot + (gw * 8 + q) * 1024), 16,
                                                      off[q], 0, 0, 0);
+    }
+    // the descriptor starts at the step's first row, so that offsets stay
+    // small however many rows there are
+    __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
+        const int row0 = step * kStep;
+        const uint32_t rows = (uint32_t)min(red - row0, kStep);
+        issue(pmake_rsrc(base + (size_t)row0 * ld, rows * ld - col0), off, slot, gw);
     }
 };
 
@@ -169,6 +148,29 @@ struct Frag {
     }
 };
 
+// A memory phase: the step's fragments from slots `a` and `b`, and `copy` into
+// slot `to`.  The three slots are different ones, and saying so matters: the
+// transposing read is known to the compiler as an access that copies in flight
+// might still change, and it would wait for all of them before each phase.
+// That a step's copies have landed is this file's waits and barriers.
+template <bool ACOL, bool BCOL, typename Copy>
+__device__ __forceinline__ bool memory_phase(bool compute, const char* __restrict__ a,
+                                             const char* __restrict__ b, char* __restrict__ to,
+                                             const Frag<ACOL, 4>& ra, const Frag<BCOL, 2>& rb,
+                                             bf16x8_t (&fa)[4][4], bf16x8_t (&fb)[4][2],
+                                             const Copy& copy) {
+    if (compute) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) fa[ks][f] = ra.read(a, f, ks);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) fb[ks][f] = rb.read(b, f, ks);
+        }
+    }
+    return copy(to);
+}
+
 // The main loop (phases and slot reuse as PingPongCore): operand B is copied by
 // waves 0-3 one step ahead into two slots, operand A by waves 4-7 two steps
 // ahead into three.
@@ -181,7 +183,7 @@ struct PingPong {
     }
 
     template <bool COMPUTE>
-    __device__ __forceinline__ void run(char* lds, const CopyA& ca, const CopyB& cb, Offsets& off,
+    __device__ __forceinline__ void run(char* lds, const CopyA& ca, const CopyB& cb, const Offsets& off,
                                         int steps, int wave, int arow0, int brow0) {
         const int lane = lane_id();
         const bool second = wave >= 4;  // wave-uniform
@@ -205,31 +207,14 @@ struct PingPong {
         rb.init(brow0, lane);
         bf16x8_t fa[4][4], fb[4][2];
 
-        int id = -1;  // slot of the step after the next copy
         barrier();
         if (!second) {
-            int id0 = -1;
-            if constexpr (CopyB::kLook) {
-                id0 = cb.fetch(0, lane);
-                id = cb.fetch(1, lane);
-                cb.place(off, id0, 0, gw, lane);
-            }
             if (steps > 0) cb.copy(off, slot_b(0), 0, gw);
-            if constexpr (CopyB::kLook) cb.place(off, id, 1, gw, lane);
             wait_vmcnt<0>();
         } else {
-            int id0 = -1, id1 = -1;
-            if constexpr (CopyA::kLook) {
-                id0 = ca.fetch(0, lane);
-                id1 = ca.fetch(1, lane);
-                id = ca.fetch(2, lane);
-                ca.place(off, id0, 0, gw, lane);
-            }
             if (steps > 0) ca.copy(off, slot_a(0), 0, gw);
             if (steps > 1) {
-                if constexpr (CopyA::kLook) ca.place(off, id1, 1, gw, lane);
                 ca.copy(off, slot_a(1), 1, gw);
-                if constexpr (CopyA::kLook) ca.place(off, id, 2, gw, lane);
                 wait_vmcnt<kInstr>();
             } else {
                 wait_vmcnt<0>();
@@ -240,28 +225,18 @@ struct PingPong {
         int asl = 0, bsl = 0;
         for (int s = 0; s < steps; ++s) {
             // ---- memory phase
-            if constexpr (COMPUTE) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) fa[ks][a] = ra.read(slot_a(asl), a, ks);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) fb[ks][b] = rb.read(slot_b(bsl), b, ks);
-                }
-            }
-            if (!second) {
-                if (s + 1 < steps) {
-                    if constexpr (CopyB::kLook) id = cb.fetch(s + 2, lane);
-                    cb.copy(off, slot_b(bsl ^ 1), s + 1, gw);
-                }
-            } else {
-                if (s + 2 < steps) {
-                    if constexpr (CopyA::kLook) id = ca.fetch(s + 3, lane);
-                    ca.copy(off, slot_a(asl == 0 ? 2 : asl - 1), s + 2, gw);
-                    wait_vmcnt<kInstr>();
-                } else {
-                    wait_vmcnt<0>();
-                }
+            const bool copied = memory_phase(
+                COMPUTE, slot_a(asl), slot_b(bsl), second ? slot_a(asl == 0 ? 2 : asl - 1) : slot_b(bsl ^ 1),
+                ra, rb, fa, fb, [&](char* to) {
+                    const int n = s + (second ? 2 : 1);
+                    if (n >= steps) return false;
+                    if (second) ca.copy(off, to, n, gw);
+                    else cb.copy(off, to, n, gw);
+                    return true;
+                });
+            if (second) {
+                if (copied) wait_vmcnt<kInstr>();
+                else wait_vmcnt<0>();
             }
             __builtin_amdgcn_s_waitcnt(0xC07F);
             barrier();
@@ -275,12 +250,7 @@ struct PingPong {
                         for (int b = 0; b < 2; ++b)
                             acc[a][b] = mfma32_bf16(fa[ks][a], fb[ks][b], acc[a][b]);
             }
-            if (!second) {
-                if constexpr (CopyB::kLook) cb.place(off, id, s + 2, gw, lane);
-                wait_vmcnt<0>();
-            } else if constexpr (CopyA::kLook) {
-                ca.place(off, id, s + 3, gw, lane);
-            }
+            if (!second) wait_vmcnt<0>();
             barrier();
             asl = asl + 1 == kASlots ? 0 : asl + 1;
             bsl ^= 1;
@@ -394,7 +364,7 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     const uint16_t* src = DX ? g.dy : g.x;
     const uint32_t how = DX ? g.how_dy : g.how_x;
     const uint32_t ld_b = (uint32_t)red * 2;
-    typedef typename std::conditional<DX, ColCopy<false>, RowCopy>::type CopyA;
+    typedef typename std::conditional<DX, ColCopy, RowCopy>::type CopyA;
     CopyA ca;
     RowCopy cb;
     Offsets off;
@@ -412,7 +382,7 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
                       (uint32_t)(by_token ? g.T : blk.rows) * ld_b);
     cb.red_bytes = ld_b;
     if (DX && wave >= 4) {
-        if constexpr (DX) ca.in_order(off, gw, lane);
+        if constexpr (DX) ColCopy::in_order(off, ca.ld, gw, lane);
     } else {
         const uint32_t chunk = RowCopy::chunk(gw, lane);
         uint32_t p[kInstr];
@@ -451,59 +421,375 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
 }
 
 // ---- weight gradient -----------------------------------------------------------------
+// An expert's reduction is its rows, often few steps long, so a tile's start
+// (the first copies' latency) and end (256 x 256 values to store) would cost as
+// much as its products.  A workgroup therefore stays for many tiles and its
+// copies run on from one tile into the next: the ring of slots knows steps
+// only, and while a tile's results are stored the next tile's first two steps
+// are in flight.  Per tile each group's phases are (memory, compute) for every
+// step and one more that stores, the second group a phase behind as above:
+//
+//   first     M0 C0 .. Ms-1 Cs-1 E    M0'  C0'
+//   second       M0 .. Cs-2 Ms-1 Cs-1 E    M0'
+//
+// Both groups stage their results through the slot of operand A's last step,
+// the only one that no copy in flight uses, 8 KB a wave: the first group's E
+// runs while the second computes from registers, the second's while the first
+// reads other slots.  Waits count in the order of issue, so a copy issued after
+// a tile's stores would land only when those are done: the first group issues
+// the one of its next memory phase before its stores (its slot is free once
+// both groups have read the tile's last step), and the second group, whose
+// copies lead by two steps, waits for all but the stores and the last copy.
+//
+// Looked-up rows: a step's slots come by scalar loads a phase before they are
+// used, their offsets are computed between the MFMAs of the compute phase.
+//
 // Tile order: each XCD takes an eighth of every expert's tiles (experts have
 // different numbers of rows; an expert to an XCD would leave most of them
 // idle), the eighths turned by one from expert to expert so that few tiles
 // spread too; within it kGroup column tiles fastest, then the n tiles.
-template <bool LOOK>
+struct DwTile {
+    int e, a0, b0, row0, rows;
+};
+struct DwWalk {
+    int a_tiles, b_tiles, tiles, per_xcd, xcd, stride, end;
+
+    __device__ __forceinline__ DwWalk(const GroupedArgs& g) {
+        a_tiles = (g.K + kTile - 1) / kTile;
+        b_tiles = (g.N + kTile - 1) / kTile;
+        tiles = a_tiles * b_tiles;
+        per_xcd = (tiles + 7) / 8;
+        xcd = (int)blockIdx.x % 8;
+        stride = (int)gridDim.x / 8;
+        end = g.E * per_xcd;
+    }
+    // the first tile at or after position `at` of this workgroup's list (with
+    // rows, if `rows_only`); at is end when there is none
+    __device__ __forceinline__ DwTile find(const GroupedArgs& g, int& at, bool rows_only) const {
+        DwTile t = {0, 0, 0, 0, 0};
+        for (; at < end; at += stride) {
+            t.e = at / per_xcd;
+            const int i = ((xcd + t.e) % 8) * per_xcd + at % per_xcd;
+            if (i >= tiles) continue;
+            t.row0 = grouped_offset_scalar(g, t.e);
+            t.rows = max(grouped_offset_scalar(g, t.e + 1) - t.row0, 0);
+            if (rows_only && t.rows == 0) continue;
+            const int span = kGroup * b_tiles, grp = i / span, in = i % span;
+            const int gsize = min(kGroup, a_tiles - grp * kGroup);
+            t.a0 = (grp * kGroup + in % gsize) * kTile;
+            t.b0 = in / gsize * kTile;
+            return t;
+        }
+        at = end;
+        return t;
+    }
+};
+// The steps of a workgroup's tiles, one after the other.
+struct DwSteps {
+    int at, step;
+    DwTile t;
+
+    __device__ __forceinline__ bool more(const DwWalk& w) const { return at < w.end; }
+    __device__ __forceinline__ void next(const GroupedArgs& g, const DwWalk& w) {
+        if (++step * kStep >= t.rows) {
+            at += w.stride;
+            t = w.find(g, at, true);
+            step = 0;
+        }
+    }
+};
+
+constexpr int kDwStores = 16;  // stores of a wave's results, at least
+
+// Rows n0.. (of at most 64) and columns k0.. (of 128) of dW[e] from a wave's
+// accumulators, through 8 KB of LDS: 32 rows of 256 bytes at a time, chunks
+// permuted by the row.  Every store is issued whatever the tile's size (what
+// lies outside is an offset out of range), so that their number is known.
+typedef __attribute__((address_space(3))) char* lds_char_t;
+
+// ds_write_b64 / b128 without the wait for copies in flight that the compiler
+// puts before a store to LDS; the caller fences
+__device__ __forceinline__ void stage(uint32_t at, uint2 v) {
+    __asm__ volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+__device__ __forceinline__ void stage(uint32_t at, f32x4_t v) {
+    __asm__ volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+// v, used from here on as if it were another value: addresses made from it are
+// computed again instead of being held in registers that the main loop needs
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+    __asm__ volatile("" : "+v"(v));
+    return v;
+}
+
+enum class DwOut { kBf16, kF32, kF32Add };
+template <DwOut OUT>
+__device__ __forceinline__ void store_dw(char* st, const f32x16_t (&acc)[4][2],
+                                         const GroupedArgs& g, int e, int n0, int k0) {
+    const int lane = late_lane();
+    const int li = lane & 31, half = lane >> 5, rr = lane >> 4, c = lane & 15;
+    constexpr int size = OUT == DwOut::kBf16 ? 2 : 4, per = 16 / size;
+    const uint32_t ld = (uint32_t)(g.K * size);
+    char* base = (char*)g.out + (((size_t)e * g.N + n0) * g.K + k0) * size;
+    const prsrc_t r = pmake_rsrc(base, (uint32_t)min(64, g.N - n0) * ld - (uint32_t)(k0 * size));
+    const uint32_t at = (uint32_t)rr * ld + (uint32_t)(c * 16);
+    // (st is 8 KB aligned: the permutations are XORs of bits 4..7)
+    const uint32_t base_st = (uint32_t)(uintptr_t)(lds_char_t)st;
+    const uint32_t put = base_st + (uint32_t)(li * 256) +
+                         (OUT == DwOut::kBf16 ? ((li & 15) << 4) + 8 * half : ((li & 15) ^ half) << 4);
+    const uint32_t get = base_st + (uint32_t)(rr * 256 + ((c ^ rr) << 4));
+    auto flush = [&](int row0, int col0) {
+        lds_wave_fence();
+        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t from = fresh(get), to = fresh(at);
+        const bool in = k0 + col0 + c * per < g.K;
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            i32x4_t v[4], was[4];
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // row 4*(i0 + i) + rr
+                v[i] = *(const __attribute__((address_space(3))) i32x4_t*)(lds_char_t)(
+                    (uintptr_t)((from ^ (uint32_t)(i << 6)) + (uint32_t)((i0 + i) * 1024)));
+                o[i] = in ? to + (uint32_t)(row0 + 4 * (i0 + i)) * ld + (uint32_t)(col0 * size)
+                          : kNowhere;
+                if constexpr (OUT == DwOut::kF32Add)
+                    was[i] = __builtin_amdgcn_raw_buffer_load_b128(r, o[i], 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (OUT == DwOut::kF32Add) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] = __float_as_int(__int_as_float(was[i][j]) + __int_as_float(v[i][j]));
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(v[i], r, o[i], 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        lds_wave_fence();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        if constexpr (OUT != DwOut::kBf16) {
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                const uint32_t w = fresh(put);
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x16_t& v = acc[2 * pass + a][b];
+                        stage(w ^ (uint32_t)((a * 8 + 2 * q) << 4),
+                              f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]});
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                flush(b * 32, pass * 64);
+            }
+        } else {
+            const uint32_t w = fresh(put);
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16_t& v = acc[a][b];
+                    stage(w ^ (uint32_t)((a * 4 + q) << 4),
+                          uint2{pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                                pack_bf16x2(v[4 * q + 2], v[4 * q + 3])});
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            flush(b * 32, 0);
+        }
+    }
+}
+
+// the same rows and columns as zeros, without LDS
+__device__ __forceinline__ void store_dw_zeros(const GroupedArgs& g, int e, int n0, int k0) {
+    const int lane = late_lane(), size = g.out_f32 ? 4 : 2;
+    char* base = (char*)g.out + (((size_t)e * g.N + n0) * g.K + k0) * size;
+    const int words = min(128, g.K - k0) * size / 4, rows = min(64, g.N - n0);
+    for (int row = 0; row < rows; ++row)
+        for (int i = lane; i < words; i += kWave)
+            reinterpret_cast<float*>(base + (size_t)row * g.K * size)[i] = 0.0f;
+}
+
+template <bool LOOK, DwOut OUT>
 __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int gw = wave & 3;
-    const int a_tiles = (g.K + kTile - 1) / kTile, b_tiles = (g.N + kTile - 1) / kTile;
-    const int tiles = a_tiles * b_tiles, per_xcd = (tiles + 7) / 8;
-    const int local = (int)blockIdx.x / 8;
-    const int e = local / per_xcd;
-    const int t = (((int)blockIdx.x + e) % 8) * per_xcd + local % per_xcd;
-    if (e >= g.E || t >= tiles) return;
-    const int span = kGroup * b_tiles;
-    const int grp = t / span, in = t % span;
-    const int gsize = min(kGroup, a_tiles - grp * kGroup);
-    const int a0 = (grp * kGroup + in % gsize) * kTile, b0 = (in / gsize) * kTile;
-    const int row0 = __builtin_amdgcn_readfirstlane(grouped_offset(g, e));
-    const int rows = max(__builtin_amdgcn_readfirstlane(grouped_offset(g, e + 1)) - row0, 0);
-    if (rows == 0 && g.accumulate) return;
-
-    // a wave copies one operand: waves 4-7 x (A), waves 0-3 dy (B)
-    const bool is_x = wave >= 4;
-    const uint16_t* p = is_x ? g.x : g.dy;
-    const int width = is_x ? g.K : g.N, first = is_x ? a0 : b0;
+    const bool second = wave >= 4;
+    const DwWalk walk(g);
+    auto slot_a = [&](int s) { return lds + s * kSlotBytes; };
+    auto slot_b = [&](int s) { return lds + (kASlots + s) * kSlotBytes; };
+    auto barrier = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // a wave copies one operand: waves 4-7 x (A) two steps ahead, waves 0-3 dy
+    // (B) one step ahead
+    const uint16_t* src = second ? g.x : g.dy;
+    const int width = second ? g.K : g.N;
     const uint32_t ld = (uint32_t)width * 2;
-    ColCopy<LOOK> copy;
-    copy.token = LOOK && (is_x ? g.how_x : g.how_dy) == kRowToken;
-    copy.base = (const char*)(p + (copy.token ? 0 : (size_t)row0 * width) + first);
-    copy.ld = ld;
-    copy.col0 = (uint32_t)first * 2;
-    copy.bytes = g.T > 0 ? (uint32_t)g.T * ld - copy.col0 : 0;
-    copy.red = rows;
-    copy.ids = g.sorted + row0;
-    copy.slots = g.slots;
-    copy.magic = g.magic;
+    const bool token = LOOK && (second ? g.how_x : g.how_dy) == kRowToken;
     Offsets off;
-    if constexpr (!LOOK) copy.in_order(off, gw, lane);
+    if constexpr (!LOOK) ColCopy::in_order(off, ld, gw, lane);
+    // slots of the rows that this wave copies next (wave-uniform scalar loads)
+    typedef const __attribute__((address_space(4))) int32_t* scalar_t;
+    int ids[LOOK ? 16 : 1];
+    DwSteps lead = {(int)blockIdx.x / 8, 0, {}};  // the step copied next
+    lead.t = walk.find(g, lead.at, true);
+    auto look = [&]() {
+        if constexpr (LOOK) {
+            if (!lead.more(walk)) return;
+            const int first = lead.step * kStep + gw * 16;
+            const scalar_t p = (scalar_t)(g.sorted + lead.t.row0);
+            if (first + 16 <= lead.t.rows) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ids[i] = p[first + i];
+            } else {  // past the last row: no slot
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    ids[i] = p[min(first + i, lead.t.rows - 1)] | (first + i < lead.t.rows ? 0 : -1);
+            }
+        }
+    };
+    // a row's place: the slot's token (a quotient, see grouped_token) or its
+    // position in the step, one of them masked out
+    const uint32_t quot = token ? g.magic : 0, self = token && !g.magic ? ~0u : 0,
+                   pos = token ? 0 : ~0u;
+    const uint32_t chunk0 = ColCopy::chunk(0, lane);
+    // offsets of copy q from its two rows' slots
+    auto place = [&](int q) {
+        if constexpr (LOOK) {
+            uint32_t o[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t p = (uint32_t)ids[2 * q + h];
+                const uint32_t at = (__umulhi(p, quot) + (p & self) + ((gw * 16 + 2 * q + h) & pos)) * ld;
+                o[h] = p < g.slots ? at : kNowhere;
+            }
+            // (the chunk from its first form each time: held for every q it would
+            // cost registers that the loop does not have)
+            off[q] = (lane >> 5 ? o[1] : o[0]) + (fresh(chunk0) ^ (uint32_t)((q & 3) << 7));
+        }
+    };
+    auto place_all = [&]() {
+#pragma unroll
+        for (int q = 0; q < kInstr; ++q) place(q);
+    };
+    // copies the lead step into `slot` and moves on; false: none left
+    auto copy_next = [&](char* slot) {
+        if (!lead.more(walk)) return false;
+        const uint32_t first = (uint32_t)(second ? lead.t.a0 : lead.t.b0);
+        const int row0 = lead.step * kStep;
+        const uint32_t rows = (uint32_t)min(lead.t.rows - row0, kStep);
+        const uint32_t all = g.T > 0 ? (uint32_t)g.T : 0;
+        const uint16_t* p = src + first + (token ? 0 : (size_t)(lead.t.row0 + row0) * width);
+        const uint32_t bytes = (token ? all : rows) * ld;
+        ColCopy::issue(pmake_rsrc(p, bytes ? bytes - first * 2 : 0), off, slot, gw);
+        lead.next(g, walk);
+        look();
+        return true;
+    };
+
     const int arow0 = (gw & 1) * 128, brow0 = (wave >> 2) * 128 + (gw >> 1) * 64;
-    const bool used = b0 + brow0 < g.N && a0 + arow0 < g.K;
-    const int steps = (rows + kStep - 1) / kStep;
-    PingPong<true, true, ColCopy<LOOK>, ColCopy<LOOK>> core;
-    if (used) core.template run<true>(lds, copy, copy, off, steps, wave, arow0, brow0);
-    else core.template run<false>(lds, copy, copy, off, steps, wave, arow0, brow0);
-    if (used) {
-        const int n = b0 + brow0 + late_lane();
-        store_tile(lds + gw * kStArea, core.acc, n < g.N ? ((long)e * g.N + n) * g.K : -1, a0 + arow0,
-                   g.K, g.out, g.out_f32, g.accumulate);
+    Frag<true, 4> ra;
+    Frag<true, 2> rb;
+    ra.init(arow0, lane);
+    rb.init(brow0, lane);
+    bf16x8_t fa[4][4], fb[4][2];
+    f32x16_t acc[4][2];
+    look();
+    place_all();
+    copy_next(second ? slot_a(0) : slot_b(0));
+    place_all();
+    if (second) {
+        copy_next(slot_a(1));
+        place_all();
     }
-    core.finish(wave);
+    wait_vmcnt<0>();
+    barrier();
+    if (second) barrier();
+    int asl = 0, bsl = 0;
+    bool stored = false;  // the phase before issued kDwStores stores or more
+    bool early = false;   // the next memory phase's copy is issued already
+    for (int at = (int)blockIdx.x / 8;; at += walk.stride) {
+        const DwTile t = walk.find(g, at, OUT == DwOut::kF32Add);
+        if (at >= walk.end) break;
+        const bool used = t.b0 + brow0 < g.N && t.a0 + arow0 < g.K;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+        for (int left = t.rows; left > 0; left -= kStep) {
+            // ---- memory phase
+            const bool copied = memory_phase(
+                used, slot_a(asl), slot_b(bsl),
+                second ? slot_a(asl == 0 ? 2 : asl - 1) : slot_b(bsl ^ 1), ra, rb, fa, fb,
+                [&](char* to) { return early || copy_next(to); });
+            if (second) {
+                // the next step has landed: only this copy, and the stores
+                // issued after the one before it, may be left
+                if (!copied) wait_vmcnt<0>();
+                else if (stored) wait_vmcnt<kInstr + kDwStores>();
+                else wait_vmcnt<kInstr>();
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            barrier();
+            // ---- compute phase
+            if (used) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            acc[a][b] = mfma32_bf16(fa[ks][a], fb[ks][b], acc[a][b]);
+                        if constexpr (LOOK) {
+                            if (a & 1) place(ks * 2 + a / 2);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+            } else {
+                place_all();
+            }
+            if (!second) {
+                // the next step has landed; its copy is older than the stores
+                if (early && stored) wait_vmcnt<kDwStores>();
+                else wait_vmcnt<0>();
+            }
+            early = stored = false;
+            barrier();
+            asl = asl + 1 == kASlots ? 0 : asl + 1;
+            bsl ^= 1;
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) pin(acc[a][b]);
+        // ---- the tile's results
+        if (!second && !early) {
+            copy_next(slot_b(bsl ^ 1));
+            early = true;
+        }
+        if (used) {
+            if (t.rows == 0) {
+                store_dw_zeros(g, t.e, t.b0 + brow0, t.a0 + arow0);
+            } else {
+                store_dw<OUT>(slot_a(asl == 0 ? 2 : asl - 1) + gw * (kSlotBytes / 4), acc, g, t.e,
+                              t.b0 + brow0, t.a0 + arow0);
+                stored = true;
+            }
+        }
+        barrier();
+    }
+    if (!second) barrier();  // for the second group's phase behind
 }
 
 }  // namespace
@@ -527,9 +813,18 @@ void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s) { launch_rows_
 
 void launch_grouped_tiles_dw(const GroupedArgs& g, hipStream_t s) {
     const long tiles = (long)((g.K + kTile - 1) / kTile) * ((g.N + kTile - 1) / kTile);
-    const int grid = (int)((tiles + 7) / 8 * 8 * g.E);
-    if (g.sorted) grouped_dw_kernel<true><<<grid, 512, 0, s>>>(g);
-    else grouped_dw_kernel<false><<<grid, 512, 0, s>>>(g);
+    const long per_xcd = (tiles + 7) / 8 * g.E;
+    const int grid = 8 * (int)(per_xcd < kCusPerXcd ? per_xcd : kCusPerXcd);
+    auto run = [&](auto look, auto out) {
+        grouped_dw_kernel<decltype(look)::value, decltype(out)::value><<<grid, 512, 0, s>>>(g);
+    };
+    auto with_out = [&](auto look) {
+        if (g.accumulate) run(look, std::integral_constant<DwOut, DwOut::kF32Add>{});
+        else if (g.out_f32) run(look, std::integral_constant<DwOut, DwOut::kF32>{});
+        else run(look, std::integral_constant<DwOut, DwOut::kBf16>{});
+    };
+    if (g.sorted) with_out(std::true_type{});
+    else with_out(std::false_type{});
 }
 
 }  // namespace moe
