@@ -9,6 +9,7 @@ current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -23,37 +24,53 @@ MOE_OUT_BF16 = 0
 MOE_OUT_FP32 = 1
 MOE_OUT_FP32_ADD = 2
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
 
 def _arg(t, name: str, dtype, shape, device):
-    """A dense GPU tensor of this dtype, shape (None: any extent) and device."""
+    """A dense GPU tensor of this dtype, shape and device.  One expression for
+    the case that everything fits: these checks run before every call, and the
+    shortest kernels here take a few microseconds."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
-        raise ValueError(f"{name} must have shape {want}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _sizes(t, name: str, dims: int):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-dimensional GPU tensor")
+    return t.shape
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _fn(name: str):
+    return getattr(load_library(), name)
+
+
 def _call(device: torch.device, name: str, *args):
     """One library call on the device's current stream, with that device
     current."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        rc = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(rc, name)
+            rc = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc, name)
 
 
 def _out(out, name: str, dtype, shape, device):
@@ -66,46 +83,62 @@ def _workspace(device, workspace, nbytes: int):
     """The caller's workspace, or one allocated here; the library checks the size."""
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _arg(workspace, "workspace", torch.uint8, (None,), device)
+    _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
     if workspace.numel() < nbytes:  # an empty one's null pointer would ask for the size
         raise MoEError(MOE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, {nbytes} needed:")
     return workspace
 
 
-def _rows(sorted_ids, expert_offsets, num_tokens, topk, gather_from, any_rows: bool, device):
-    """Checks the row arguments; returns (E, T).  gather_from: a gathered
-    operand (its rows are the tokens), or None."""
-    E = expert_offsets.shape[0] - 1 if expert_offsets.dim() == 1 else 0
-    _arg(expert_offsets, "expert_offsets", torch.int32, (None,), device)
+@functools.lru_cache(maxsize=256)
+def _dw_workspace(*sizes) -> int:
+    nbytes = ctypes.c_size_t(0)
+    _check(_fn("moe_grouped_gemm_dw")(None, None, None, None, *sizes, None, None,
+                                      ctypes.byref(nbytes), None),
+           "moe_grouped_gemm_dw (size query)")
+    return nbytes.value
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(kind: int, M: int, K: int, topk: int, du_topk: int) -> int:
+    nbytes = ctypes.c_size_t(0)
+    _check(_fn("moe_block_norm_bwd")(*[None] * 9, kind, M, K, topk, du_topk, 1.0, *[None] * 6,
+                                     ctypes.byref(nbytes), None),
+           "moe_block_norm_bwd (size query)")
+    return nbytes.value
+
+
+def _rows(sorted_ids, expert_offsets, num_tokens, gather_from, any_rows: bool, E: int, device):
+    """Checks the row arguments; returns T.  gather_from: the rows of a
+    gathered operand (the tokens), or None."""
+    _arg(expert_offsets, "expert_offsets", _I32, (E + 1,), device)
     if sorted_ids is None:
         if any_rows:
             raise ValueError("gather and scatter need sorted_ids")
-        return E, 0
-    _arg(sorted_ids, "sorted_ids", torch.int32, (None,), device)
+        return 0
+    _arg(sorted_ids, "sorted_ids", _I32, (sorted_ids.numel(),), device)
     if gather_from is not None:
-        if num_tokens is not None and num_tokens != gather_from.shape[0]:
+        if num_tokens is not None and num_tokens != gather_from:
             raise ValueError(f"num_tokens is {num_tokens}, the gathered operand has "
-                             f"{gather_from.shape[0]} rows")
-        return E, gather_from.shape[0]
+                             f"{gather_from} rows")
+        return gather_from
     if num_tokens is None:
         raise ValueError("num_tokens is needed with sorted_ids when nothing is gathered")
-    return E, int(num_tokens)
+    return int(num_tokens)
 
 
 def _product(name, rows_in, w, expert_offsets, sorted_ids, topk, num_tokens, gather, scatter, out,
              dx: bool):
+    E, N, K = _sizes(w, "w", 3)
     dev = w.device
-    _arg(w, "w", torch.bfloat16, (None, None, None), None)
-    E, N, K = w.shape
-    _arg(rows_in, "dy" if dx else "x", torch.bfloat16, (None, N if dx else K), dev)
-    En, T = _rows(sorted_ids, expert_offsets, num_tokens, topk, rows_in if gather else None,
-                  gather or scatter, dev)
-    if En != E:
-        raise ValueError(f"expert_offsets must have {E + 1} entries, got {En + 1}")
-    R = rows_in.shape[0] if sorted_ids is None else sorted_ids.shape[0]
-    if not gather and rows_in.shape[0] != R:
-        raise ValueError(f"the operand has {rows_in.shape[0]} rows, sorted_ids {R}")
-    out = _out(out, "out", torch.bfloat16, (T * topk if scatter else R, K if dx else N), dev)
+    _arg(w, "w", _BF16, (E, N, K), dev)
+    count, _ = _sizes(rows_in, "dy" if dx else "x", 2)
+    _arg(rows_in, "dy" if dx else "x", _BF16, (count, N if dx else K), dev)
+    T = _rows(sorted_ids, expert_offsets, num_tokens, count if gather else None,
+              gather or scatter, E, dev)
+    R = count if sorted_ids is None else sorted_ids.shape[0]
+    if not gather and count != R:
+        raise ValueError(f"the operand has {count} rows, sorted_ids {R}")
+    out = _out(out, "out", _BF16, (T * topk if scatter else R, K if dx else N), dev)
     rows = (MOE_ROWS_GATHER if gather else 0) | (MOE_ROWS_SCATTER if scatter else 0)
     _call(dev, name, _p(rows_in), _p(w), _p(expert_offsets), _p(sorted_ids), rows, T, topk, R, E,
           K, N, _p(out))
@@ -149,34 +182,31 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     moe_grouped_gemm's weights: [E,N,K] in ``out_dtype`` (bf16 or fp32), or
     into ``out``; ``accumulate`` adds to an fp32 ``out``.  gather_dy /
     gather_x: that operand has num_tokens rows, read by the rows' tokens."""
+    ny, N = _sizes(dy, "dy", 2)
+    nx, K = _sizes(x, "x", 2)
     dev = dy.device
-    _arg(dy, "dy", torch.bfloat16, (None, None), None)
-    _arg(x, "x", torch.bfloat16, (None, None), dev)
-    if gather_dy and gather_x and dy.shape[0] != x.shape[0]:
+    _arg(dy, "dy", _BF16, (ny, N), dev)
+    _arg(x, "x", _BF16, (nx, K), dev)
+    if gather_dy and gather_x and ny != nx:
         raise ValueError("two gathered operands must have the same number of rows")
-    E, T = _rows(sorted_ids, expert_offsets, num_tokens, topk,
-                 x if gather_x else dy if gather_dy else None, gather_dy or gather_x, dev)
-    N, K = dy.shape[1], x.shape[1]
-    R = dy.shape[0] if sorted_ids is None else sorted_ids.shape[0]
-    for t, name, gathered in ((dy, "dy", gather_dy), (x, "x", gather_x)):
-        if not gathered and t.shape[0] != R:
-            raise ValueError(f"{name} must have {R} rows, got {t.shape[0]}")
+    E = _sizes(expert_offsets, "expert_offsets", 1)[0] - 1
+    T = _rows(sorted_ids, expert_offsets, num_tokens, nx if gather_x else ny if gather_dy else None,
+              gather_dy or gather_x, E, dev)
+    R = ny if sorted_ids is None else sorted_ids.shape[0]
+    for count, name, gathered in ((ny, "dy", gather_dy), (nx, "x", gather_x)):
+        if not gathered and count != R:
+            raise ValueError(f"{name} must have {R} rows, got {count}")
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"the gradient must be bfloat16 or float32, got {out_dtype}")
-    if accumulate and (out is None or out_dtype != torch.float32):
+    if accumulate and (out is None or out_dtype is not _F32):
         raise ValueError("accumulate needs a float32 out")
     out = _out(out, "out", out_dtype, (E, N, K), dev)
-    mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype == torch.float32 \
-        else MOE_OUT_BF16
+    mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype is _F32 else MOE_OUT_BF16
     rows = (MOE_ROWS_GATHER if gather_x else 0) | (MOE_ROWS_GATHER_DY if gather_dy else 0)
-    nbytes = ctypes.c_size_t(0)
     sizes = (rows, T, topk, R, E, K, N, mode)
-    _check(load_library().moe_grouped_gemm_dw(None, None, None, None, *sizes, None, None,
-                                              ctypes.byref(nbytes), None),
-           "moe_grouped_gemm_dw (size query)")
-    workspace = _workspace(dev, workspace, nbytes.value)
+    workspace = _workspace(dev, workspace, _dw_workspace(*sizes))
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, "moe_grouped_gemm_dw", _p(dy), _p(x), _p(expert_offsets), _p(sorted_ids), *sizes,
           _p(out), _p(workspace), ctypes.byref(nbytes))
@@ -184,23 +214,23 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
 
 
 def _gated(g, topk_weights, sorted_ids, num_rows):
+    R, two_n = _sizes(g, "g", 2)
     dev = g.device
-    _arg(g, "g", torch.bfloat16, (None, None), None)
-    R, two_n = g.shape
+    _arg(g, "g", _BF16, (R, two_n), dev)
     if two_n % 2:
         raise ValueError("g must have an even number of columns (gate, up)")
     slots = 0
     if topk_weights is not None:
-        _arg(topk_weights, "topk_weights", torch.float32, (None,) * topk_weights.dim(), dev)
+        _arg(topk_weights, "topk_weights", _F32, topk_weights.shape, dev)
         slots = topk_weights.numel()
         if sorted_ids is None and slots != R:
             raise ValueError(f"without sorted_ids topk_weights must have {R} values, got {slots}")
     if sorted_ids is not None:
-        _arg(sorted_ids, "sorted_ids", torch.int32, (R,), dev)
+        _arg(sorted_ids, "sorted_ids", _I32, (R,), dev)
         if topk_weights is None:
             raise ValueError("sorted_ids is for topk_weights")
     if num_rows is not None:
-        _arg(num_rows, "num_rows", torch.int32, (1,), dev)
+        _arg(num_rows, "num_rows", _I32, (1,), dev)
     return dev, R, two_n // 2, slots
 
 
@@ -213,7 +243,7 @@ def moe_silu_mul(g: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *
     sorted_ids, 1 without weights).  Padding rows are zero; rows at and past
     num_rows (moe_align's num_padded) are not written."""
     dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
-    out = _out(out, "out", torch.bfloat16, (R, N), dev)
+    out = _out(out, "out", _BF16, (R, N), dev)
     _call(dev, "moe_silu_mul", _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows), slots, R, N,
           _p(out))
     return out
@@ -227,7 +257,7 @@ def moe_silu_mul_bwd(da: torch.Tensor, g: torch.Tensor,
     topk_weights' shape, or None without weights).  Weights of slots that no
     row names get an uninitialised gradient."""
     dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
-    _arg(da, "da", torch.bfloat16, (R, N), dev)
+    _arg(da, "da", _BF16, (R, N), dev)
     dg = torch.empty_like(g)
     dw = None if topk_weights is None else torch.empty_like(topk_weights)
     _call(dev, "moe_silu_mul_bwd", _p(da), _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows),
@@ -258,24 +288,25 @@ def moe_block_norm(h: torch.Tensor, o: Optional[torch.Tensor] = None,
     h_out and may be h."""
     kind = _stream_type(h, "h")
     dev = h.device
-    M, K = _arg(h, "h", h.dtype, (None, None), None).shape
+    M, K = _sizes(h, "h", 2)
+    _arg(h, "h", h.dtype, (M, K), dev)
     if w_pre is not None:
-        _arg(w_pre, "w_pre", torch.float32, (K,), dev)
+        _arg(w_pre, "w_pre", _F32, (K,), dev)
     if o is None:
         if gate is not None or w_post is not None or out is not None:
             raise ValueError("gate, w_post and out are for a block's output o")
         if w_pre is None:
             raise ValueError("one of o and w_pre is needed")
     else:
-        _arg(o, "o", torch.bfloat16, (M * topk, K), dev)
+        _arg(o, "o", _BF16, (M * topk, K), dev)
         if gate is not None:
-            _arg(gate, "gate", torch.float32, (M,), dev)
+            _arg(gate, "gate", _F32, (M,), dev)
         if w_post is not None:
-            _arg(w_post, "w_post", torch.float32, (K,), dev)
+            _arg(w_post, "w_post", _F32, (K,), dev)
         out = _out(out, "out", h.dtype, (M, K), dev)
-    u = None if w_pre is None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    r1 = None if w_post is None else torch.empty(M, dtype=torch.float32, device=dev)
-    r2 = None if w_pre is None else torch.empty(M, dtype=torch.float32, device=dev)
+    u = None if w_pre is None else torch.empty((M, K), dtype=_BF16, device=dev)
+    r1 = None if w_post is None else torch.empty(M, dtype=_F32, device=dev)
+    r2 = None if w_pre is None else torch.empty(M, dtype=_F32, device=dev)
     _call(dev, "moe_block_norm", _p(h), _p(o), _p(gate), _p(w_post), _p(w_pre), kind, M, K, topk,
           res_scale, eps, _p(out), _p(u), _p(r1), _p(r2))
     return (h if o is None else out), u, r1, r2
@@ -298,7 +329,8 @@ def moe_block_norm_bwd(dh_out: Optional[torch.Tensor], du: Optional[torch.Tensor
     none."""
     kind = _stream_type(h_out, "h_out")
     dev = h_out.device
-    M, K = _arg(h_out, "h_out", h_out.dtype, (None, None), None).shape
+    M, K = _sizes(h_out, "h_out", 2)
+    _arg(h_out, "h_out", h_out.dtype, (M, K), dev)
     if dh_out is not None:
         _arg(dh_out, "dh_out", h_out.dtype, (M, K), dev)
     if (w_pre is None) != (du is None) or (w_pre is None) != (rstd_pre is None):
@@ -306,33 +338,29 @@ def moe_block_norm_bwd(dh_out: Optional[torch.Tensor], du: Optional[torch.Tensor
     if (w_post is None) != (rstd_post is None):
         raise ValueError("w_post and rstd_post go together")
     if w_pre is not None:
-        _arg(w_pre, "w_pre", torch.float32, (K,), dev)
-        _arg(du, "du", torch.bfloat16, (M * du_topk, K), dev)
-        _arg(rstd_pre, "rstd_pre", torch.float32, (M,), dev)
+        _arg(w_pre, "w_pre", _F32, (K,), dev)
+        _arg(du, "du", _BF16, (M * du_topk, K), dev)
+        _arg(rstd_pre, "rstd_pre", _F32, (M,), dev)
     elif dh_out is None or o is None:
         raise ValueError("nothing to differentiate: give du, or dh_out and o")
     if o is None:
         if gate is not None or w_post is not None:
             raise ValueError("gate and w_post are for a block's output o")
     else:
-        _arg(o, "o", torch.bfloat16, (M * topk, K), dev)
+        _arg(o, "o", _BF16, (M * topk, K), dev)
         if gate is not None:
-            _arg(gate, "gate", torch.float32, (M,), dev)
+            _arg(gate, "gate", _F32, (M,), dev)
         if w_post is not None:
-            _arg(w_post, "w_post", torch.float32, (K,), dev)
-            _arg(rstd_post, "rstd_post", torch.float32, (M,), dev)
+            _arg(w_post, "w_post", _F32, (K,), dev)
+            _arg(rstd_post, "rstd_post", _F32, (M,), dev)
 
-    def new(like, shape, dtype=torch.float32):
+    def new(like, shape, dtype=_F32):
         return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
 
     dh = torch.empty_like(h_out)
-    do = new(o, (M, K), torch.bfloat16)
+    do = new(o, (M, K), _BF16)
     dgate, dw_post, dw_pre = new(gate, M), new(w_post, K), new(w_pre, K)
-    nbytes = ctypes.c_size_t(0)
-    _check(load_library().moe_block_norm_bwd(*[None] * 9, kind, M, K, topk, du_topk, res_scale,
-                                             *[None] * 6, ctypes.byref(nbytes), None),
-           "moe_block_norm_bwd (size query)")
-    workspace = _workspace(dev, workspace, nbytes.value)
+    workspace = _workspace(dev, workspace, _norm_workspace(kind, M, K, topk, du_topk))
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, "moe_block_norm_bwd", _p(dh_out), _p(du), _p(h_out), _p(o), _p(gate), _p(w_post),
           _p(w_pre), _p(rstd_post), _p(rstd_pre), kind, M, K, topk, du_topk, res_scale, _p(dh),
