@@ -11,6 +11,7 @@
 // neighbours in memory) and "B" (the other one).  Row lookups (gather by
 // token, scatter by slot) happen in the kernels; sums are fp32.
 #include "grouped.hpp"
+#include "tiles.hpp"
 
 namespace moe {
 
@@ -19,35 +20,93 @@ namespace {
 constexpr int kOpFwd = 0, kOpDx = 1, kOpDw = 2;
 
 // ---------------------------------------------------------------------------
-// Any widths: 64 x 64 outputs per workgroup of four waves, 32 reduction
-// elements a step, element loads guarded one by one and staged through
-// registers into LDS rows of 32 + 8 elements (the pad spreads the 16 rows of
-// an operand read over the banks).  16x16x32 MFMA: lane l supplies row
-// l % 16, reduction 8*(l/16)..+8; its accumulators are rows 4*(l/16)+v of
-// column l % 16.
+// Small tiles, any widths: 64 x 64 outputs per workgroup of four waves (32 x 32
+// each, 16x16x32 MFMAs), 64 reduction elements a step.  For products with too
+// few outputs for 256 x 256 tiles, where the time is the latency of a step, and
+// for rows that are not whole 16-byte chunks, which the copies of those tiles
+// cannot take.  A step's chunks of 8 elements are loaded into registers two
+// steps ahead (16 bytes at any 2-byte address; a row's last chunk element by
+// element, so that nothing past a row is read) and stored to one of two LDS
+// buffers, a barrier a step.
+//
+// LDS layouts, both 64 rows of 128 bytes.  Rows along the output (operands that
+// are contiguous in the reduction): 16-byte chunks permuted by the row as in
+// the full tiles, fragments read directly.  Rows along the reduction: fragments
+// come through the transposing read (lane i of 16 gets column i of four rows,
+// that is 32 bytes of each), 32-byte pieces permuted so that the two times four
+// rows of a half-wave's read fall in different banks.
+//
+// 16x16x32: lane l supplies row l % 16, reduction 8*(l/16)..+8; its
+// accumulators are rows 4*(l/16)+v of column l % 16.
 // ---------------------------------------------------------------------------
-constexpr int kSimTile = 64, kSimStep = 32, kSimRow = kSimStep + 8;
+constexpr int kSim = 64;                       // tile and step
+constexpr int kSimBytes = kSim * kSim * 2;     // one operand's step
+constexpr int kSimAhead = 2;                   // steps loaded ahead
+
+typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
+typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
+
+// columns c..c+7 of a row of `width`; zeros past its end and for no row
+__device__ __forceinline__ u16x8_t load_chunk(const uint16_t* row, int c, int width) {
+    u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!row) return v;
+    if (c + 8 <= width) return *reinterpret_cast<const u16x8_any_t*>(row + c);
+    if (c < width) {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (c + i < width) v[i] = row[c + i];
+    }
+    return v;
+}
+
+// chunk c (of 8) of row r, by layout
+template <bool COL>
+__device__ __forceinline__ int sim_at(int r, int c) {
+    if constexpr (COL) {
+        const int x = ((r >> 1) & 1) | (((r >> 3) & 1) << 1);
+        return r * 128 + ((((c >> 1) ^ x) << 1 | (c & 1)) << 4);
+    } else {
+        return r * 128 + ((c ^ swz<8>(r)) << 4);
+    }
+}
+// the fragment of 16 output rows / columns from `first`, k-slice ks
+template <bool COL>
+__device__ __forceinline__ bf16x8_t sim_frag(const char* buf, int first, int ks, int lane) {
+    if constexpr (COL) {
+        typedef short s16x4_t __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4_t* lp_t;
+        const int q = lane >> 4, j = lane & 15;
+        const int x = ((j >> 3) & 1) | ((q & 1) << 1);
+        const char* p = buf + (ks * 32 + 8 * q + (j >> 2)) * 128 + (((first >> 4) ^ x) << 5) + (j & 3) * 8;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp_t)p);
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp_t)(p + 4 * 128));
+        return bf16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    } else {
+        return *reinterpret_cast<const bf16x8_t*>(buf + sim_at<false>(first + (lane & 15), ks * 4 + (lane >> 4)));
+    }
+}
 
 template <int OP>
-__global__ __launch_bounds__(256, 4) void grouped_any_kernel(GroupedArgs g) {
-    __shared__ __attribute__((aligned(16))) uint16_t la[kSimTile * kSimRow];
-    __shared__ __attribute__((aligned(16))) uint16_t lb[kSimTile * kSimRow];
+__global__ __launch_bounds__(256, 4) void grouped_small_kernel(GroupedArgs g) {
+    constexpr bool ACOL = OP != kOpFwd, BCOL = OP == kOpDw;
+    __shared__ __attribute__((aligned(16))) char lds[2][2 * kSimBytes];
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int a_dim = OP == kOpFwd ? g.N : g.K;
-    const int a_tiles = (a_dim + kSimTile - 1) / kSimTile;
-    const int a0 = ((int)blockIdx.x % a_tiles) * kSimTile;  // first output column
+    const int a_tiles = (a_dim + kSim - 1) / kSim;
+    const int a0 = ((int)blockIdx.x % a_tiles) * kSim;  // first output column
     const int bt = (int)blockIdx.x / a_tiles;
     int e, row0, rows, b0 = 0, red;
     if constexpr (OP == kOpDw) {
-        const int n_tiles = (g.N + kSimTile - 1) / kSimTile;
+        const int n_tiles = (g.N + kSim - 1) / kSim;
         e = bt / n_tiles;
-        b0 = (bt % n_tiles) * kSimTile;
-        row0 = grouped_offset(g, e);
-        rows = max(grouped_offset(g, e + 1) - row0, 0);
+        b0 = (bt % n_tiles) * kSim;
+        row0 = grouped_offset_scalar(g, e);
+        rows = max(grouped_offset_scalar(g, e + 1) - row0, 0);
         red = rows;
+        if (rows == 0 && g.accumulate) return;
     } else {
-        const GroupedBlock b = grouped_find(grouped_scan(g, kSimTile), bt, kSimTile);
+        const GroupedBlock b = grouped_find(grouped_scan(g, kSim), bt, kSim);
         if (b.e < 0) return;
         e = b.e;
         row0 = b.row0;
@@ -55,88 +114,129 @@ __global__ __launch_bounds__(256, 4) void grouped_any_kernel(GroupedArgs g) {
         red = OP == kOpFwd ? g.K : g.N;
     }
     const uint16_t* w = g.w + (size_t)e * g.N * g.K;
-    const int b_rows = OP == kOpDw ? min(g.N - b0, kSimTile) : rows;
+    const int b_rows = OP == kOpDw ? min(g.N - b0, kSim) : rows;
 
-    f32x4_t acc[4];
+    // this thread's chunk c of rows r and r + 32 of either operand
+    const int r = tid >> 3, c = tid & 7;
+    const uint16_t* brow[2] = {nullptr, nullptr};  // fwd, dx: fixed rows of B
+    if constexpr (OP != kOpDw) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = f32x4_t{0, 0, 0, 0};
-    for (int r0 = 0; r0 < red; r0 += kSimStep) {
-        // Element (i, r) of each tile; consecutive threads take consecutive
-        // elements of the operand's contiguous dimension.
-#pragma unroll
-        for (int q = 0; q < kSimTile * kSimStep / 256; ++q) {
-            const int t = q * 256 + tid;
-            // operand A: reduction-contiguous for fwd, output-contiguous else
-            {
-                const int i = OP == kOpFwd ? t / kSimStep : t % kSimTile;
-                const int r = OP == kOpFwd ? t % kSimStep : t / kSimTile;
-                uint16_t v = 0;
-                if (a0 + i < a_dim && r0 + r < red) {
-                    if constexpr (OP == kOpFwd) {
-                        v = w[(size_t)(a0 + i) * g.K + r0 + r];
-                    } else if constexpr (OP == kOpDx) {
-                        v = w[(size_t)(r0 + r) * g.K + a0 + i];
-                    } else {
-                        const int row = grouped_row(g, row0 + r0 + r, g.how_x);
-                        if (row >= 0) v = g.x[(size_t)row * g.K + a0 + i];
-                    }
-                }
-                la[i * kSimRow + r] = v;
-            }
-            {
-                const int j = OP == kOpDw ? t % kSimTile : t / kSimStep;
-                const int r = OP == kOpDw ? t / kSimTile : t % kSimStep;
-                uint16_t v = 0;
-                if (j < b_rows && r0 + r < red) {
-                    if constexpr (OP == kOpDw) {
-                        const int row = grouped_row(g, row0 + r0 + r, g.how_dy);
-                        if (row >= 0) v = g.dy[(size_t)row * g.N + b0 + j];
-                    } else {
-                        const int row = grouped_row(g, row0 + j, OP == kOpFwd ? g.how_x : g.how_dy);
-                        if (row >= 0)
-                            v = (OP == kOpFwd ? g.x : g.dy)[(size_t)row * red + r0 + r];
-                    }
-                }
-                lb[j * kSimRow + r] = v;
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int j = r + 32 * h;
+            const int row = j < rows ? grouped_row(g, row0 + j, OP == kOpFwd ? g.how_x : g.how_dy) : -1;
+            if (row >= 0) brow[h] = (OP == kOpFwd ? g.x : g.dy) + (size_t)row * red;
         }
-        __syncthreads();
-        const int li = lane & 15, q = lane >> 4;
-        const bf16x8_t fb = *reinterpret_cast<const bf16x8_t*>(&lb[(wave * 16 + li) * kSimRow + 8 * q]);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const bf16x8_t fa = *reinterpret_cast<const bf16x8_t*>(&la[(a * 16 + li) * kSimRow + 8 * q]);
-            acc[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, fb, acc[a], 0, 0, 0);
-        }
-        __syncthreads();
     }
-    // column j = wave*16 + lane%16 of B, rows a*16 + 4*(lane/16) + v of A
-    const int j = wave * 16 + (lane & 15);
-    if (j >= b_rows) return;
-    size_t dst;
-    if constexpr (OP == kOpDw) {
-        dst = ((size_t)e * g.N + b0 + j) * g.K;
-    } else {
-        int row = row0 + j;
-        if (g.how_out == kRowSlot) {
-            row = grouped_row(g, row, kRowSlot);
-            if (row < 0) return;
-        }
-        dst = (size_t)row * a_dim;
-    }
+    struct Step { u16x8_t a[2], b[2]; };
+    auto load = [&](int step) {
+        Step s;
+        const int r0 = step * kSim;
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int c = a0 + a * 16 + 4 * (lane >> 4) + v;
-            if (c >= a_dim) continue;
-            if (g.out_f32) {
-                float* o = (float*)g.out + dst + c;
-                *o = g.accumulate ? *o + acc[a][v] : acc[a][v];
+        for (int h = 0; h < 2; ++h) {
+            const int i = r + 32 * h;
+            if constexpr (OP == kOpDw) {
+                const bool ok = r0 + i < red;
+                const int rx = ok ? grouped_row(g, row0 + r0 + i, g.how_x) : -1;
+                const int ry = ok ? grouped_row(g, row0 + r0 + i, g.how_dy) : -1;
+                s.a[h] = load_chunk(rx < 0 ? nullptr : g.x + (size_t)rx * g.K, a0 + c * 8, g.K);
+                s.b[h] = load_chunk(ry < 0 ? nullptr : g.dy + (size_t)ry * g.N, b0 + c * 8, g.N);
             } else {
-                ((uint16_t*)g.out)[dst + c] = f32_to_bf16_bits(acc[a][v]);
+                if constexpr (OP == kOpFwd)
+                    s.a[h] = load_chunk(a0 + i < g.N ? w + (size_t)(a0 + i) * g.K : nullptr, r0 + c * 8, red);
+                else
+                    s.a[h] = load_chunk(r0 + i < red ? w + (size_t)(r0 + i) * g.K : nullptr, a0 + c * 8, g.K);
+                s.b[h] = load_chunk(brow[h], r0 + c * 8, red);
             }
         }
+        return s;
+    };
+    const int fa0 = (wave & 1) * 32, fb0 = (wave >> 1) * 32;
+    f32x4_t acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
+    const int steps = (red + kSim - 1) / kSim;
+    Step ahead[kSimAhead];
+#pragma unroll
+    for (int i = 0; i < kSimAhead; ++i)
+        if (i < steps) ahead[i] = load(i);
+    for (int s0 = 0; s0 < steps; s0 += kSimAhead) {
+#pragma unroll
+        for (int i = 0; i < kSimAhead; ++i) {
+            const int s = s0 + i;
+            if (s >= steps) break;
+            char* buf = lds[s & 1];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<u16x8_t*>(buf + sim_at<ACOL>(r + 32 * h, c)) = ahead[i].a[h];
+                *reinterpret_cast<u16x8_t*>(buf + kSimBytes + sim_at<BCOL>(r + 32 * h, c)) = ahead[i].b[h];
+            }
+            // the buffer written next was last read before this barrier
+            __syncthreads();
+            if (s + kSimAhead < steps) ahead[i] = load(s + kSimAhead);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8_t fa[2], fb[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    fa[f] = sim_frag<ACOL>(buf, fa0 + 16 * f, ks, lane);
+                    fb[f] = sim_frag<BCOL>(buf + kSimBytes, fb0 + 16 * f, ks, lane);
+                }
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int j = fb0 + 16 * b + (lane & 15);
+        if (j >= b_rows) continue;
+        size_t dst;
+        if constexpr (OP == kOpDw) {
+            dst = ((size_t)e * g.N + b0 + j) * g.K;
+        } else {
+            int row = row0 + j;
+            if (g.how_out == kRowSlot) {
+                row = grouped_row(g, row, kRowSlot);
+                if (row < 0) continue;
+            }
+            dst = (size_t)row * a_dim;
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const int col = a0 + fa0 + 16 * a + 4 * (lane >> 4);
+            f32x4_t v = acc[a][b];
+            typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
+            typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
+            if (OP == kOpDw && g.out_f32) {
+                float* o = (float*)g.out + dst + col;
+                if (col + 4 <= a_dim) {
+                    f32x4_any_t* p = reinterpret_cast<f32x4_any_t*>(o);
+                    *p = g.accumulate ? *p + v : v;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (col + i < a_dim) o[i] = g.accumulate ? o[i] + v[i] : v[i];
+                }
+            } else {
+                uint16_t* o = (uint16_t*)g.out + dst + col;
+                u16x4_t q;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = f32_to_bf16_bits(v[i]);
+                if (col + 4 <= a_dim) {
+                    *reinterpret_cast<u16x4_any_t*>(o) = q;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (col + i < a_dim) o[i] = q[i];
+                }
+            }
+        }
+    }
 }
 
 int blocks_bound(const GroupedArgs& g, int B) {
@@ -144,11 +244,10 @@ int blocks_bound(const GroupedArgs& g, int B) {
 }
 
 template <int OP>
-void launch_any(const GroupedArgs& g, hipStream_t s) {
-    const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + kSimTile - 1) / kSimTile;
-    const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSimTile - 1) / kSimTile)
-                                    : blocks_bound(g, kSimTile);
-    grouped_any_kernel<OP><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+void launch_small(const GroupedArgs& g, hipStream_t s) {
+    const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + kSim - 1) / kSim;
+    const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSim - 1) / kSim) : blocks_bound(g, kSim);
+    grouped_small_kernel<OP><<<a_tiles * b_tiles, 256, 0, s>>>(g);
 }
 
 }  // namespace
@@ -158,16 +257,16 @@ static bool tiles_fit(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 
 
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
     if (tiles_fit(g)) launch_grouped_tiles_fwd(g, s);
-    else launch_any<kOpFwd>(g, s);
+    else launch_small<kOpFwd>(g, s);
 }
 void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {
     if (tiles_fit(g)) launch_grouped_tiles_dx(g, s);
-    else launch_any<kOpDx>(g, s);
+    else launch_small<kOpDx>(g, s);
 }
 size_t grouped_dw_workspace(const GroupedArgs&) { return 0; }
 void launch_grouped_dw(const GroupedArgs& g, void*, hipStream_t s) {
     if (tiles_fit(g)) launch_grouped_tiles_dw(g, s);
-    else launch_any<kOpDw>(g, s);
+    else launch_small<kOpDw>(g, s);
 }
 
 }  // namespace moe
