@@ -63,6 +63,7 @@ moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int3
     g->K = K;
     g->N = N;
     g->out_f32 = g->accumulate = 0;
+    g->splits = 1;
     g->out = nullptr;
     return MOE_OK;
 }

@@ -332,24 +332,36 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
     }
 }
 
-// dw[k] = sum of the partial rows, 64 columns a workgroup, four threads a
-// column each adding every fourth row in ascending order
-__global__ __launch_bounds__(256) void norm_parts_kernel(const float* post, const float* pre,
-                                                         int parts, int K, float* dw_post,
-                                                         float* dw_pre) {
-    __shared__ float sums[4][64];
+// dw[k] = sum of the partial rows: 32 columns a workgroup, 16 threads a column
+// each adding every 16th row in ascending order, then the 16 sums in order
+constexpr int kPartCols = 32, kPartRows = 16;
+__global__ __launch_bounds__(kPartCols * kPartRows) void norm_parts_kernel(
+    const float* post, const float* pre, int parts, int K, float* dw_post, float* dw_pre) {
+    __shared__ float sums[kPartRows][kPartCols];
     const float* src = blockIdx.y ? pre : post;
     float* dst = blockIdx.y ? dw_pre : dw_post;
     if (!dst) return;
-    const int col = (int)blockIdx.x * 64 + (int)threadIdx.x % 64, q = (int)threadIdx.x / 64;
+    const int c = (int)threadIdx.x % kPartCols, q = (int)threadIdx.x / kPartCols;
+    const int col = (int)blockIdx.x * kPartCols + c;
     float s = 0.0f;
-    if (col < K)
-        for (int p = q; p < parts; p += 4) s += src[(size_t)p * K + col];
-    sums[q][threadIdx.x % 64] = s;
+    if (col < K) {
+        int p = q;
+        for (; p + 7 * kPartRows < parts; p += 8 * kPartRows) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = src[(size_t)(p + i * kPartRows) * K + col];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; p < parts; p += kPartRows) s += src[(size_t)p * K + col];
+    }
+    sums[q][c] = s;
     __syncthreads();
-    if (q == 0 && col < K)
-        dst[col] = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
-                   (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+    if (q == 0 && col < K) {
+#pragma unroll
+        for (int i = 1; i < kPartRows; ++i) s += sums[i][c];
+        dst[col] = s;
+    }
 }
 
 // Threads, columns per load and column groups that hold a row of K columns in
@@ -397,8 +409,8 @@ void launch_block_norm_bwd(const NormArgs& a, float* partials, hipStream_t s) {
             else block_norm_bwd_kernel<TH, V, C, false><<<parts, TH, 0, s>>>(a, post, pre);
         });
     if (post || pre)
-        norm_parts_kernel<<<dim3((a.K + 63) / 64, 2), 256, 0, s>>>(post, pre, parts, a.K, a.dw_post,
-                                                                    a.dw_pre);
+        norm_parts_kernel<<<dim3((a.K + kPartCols - 1) / kPartCols, 2), kPartCols * kPartRows, 0, s>>>(
+            post, pre, parts, a.K, a.dw_post, a.dw_pre);
 }
 
 }  // namespace moe

@@ -253,19 +253,40 @@ void launch_small(const GroupedArgs& g, hipStream_t s) {
 }  // namespace
 
 // full tiles: every row of an operand is whole 16-byte chunks
-static bool tiles_fit(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
+static bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
+
+// Row products on full tiles, one a CU, unless the small tiles are few: up to
+// two a CU their shorter step wins (about 0.6-1 us against 1.3-1.5 us), beyond
+// it the larger tiles' reuse does.  us, small / full tiles, T tokens x k over E
+// experts (in brackets: small tiles):
+//   fwd N x K  1x2/16 16384x4096 [512] 44.9/54.4;  512x2/8 2048x1024 [512] 16.9/21.8;
+//              64x2/8 14336x4096 [1792] 204/160;  2048x2/8 2048x1024 [2048] 42.3/25.6
+//   dx  N x K  8x2/8 28672x4096 [512] 349/409;  128x2/8 14336x4096 [512] 199/214;
+//              256x2/8 14336x4096 [512] 253/237;  2048x2/8 1024x256 [256] 15.3/23.6;
+//              2048x2/8 2048x1024 [1024] 52.4/40.6;  8192x2/8 512x256 [1024] 19.4/17.0
+// (the weight gradient: full tiles are at least as fast throughout).
+static bool full_tiles(const GroupedArgs& g, int cols) {
+    if (!chunked(g)) return false;
+    const long experts = g.R < g.E ? g.R : g.E, blocks = g.R / kSim;
+    return (long)((cols + kSim - 1) / kSim) * (blocks > experts ? blocks : experts) > 512;
+}
 
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
-    if (tiles_fit(g)) launch_grouped_tiles_fwd(g, s);
+    if (full_tiles(g, g.N)) launch_grouped_tiles_fwd(g, s);
     else launch_small<kOpFwd>(g, s);
 }
 void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {
-    if (tiles_fit(g)) launch_grouped_tiles_dx(g, s);
+    if (full_tiles(g, g.K)) launch_grouped_tiles_dx(g, s);
     else launch_small<kOpDx>(g, s);
 }
-size_t grouped_dw_workspace(const GroupedArgs&) { return 0; }
-void launch_grouped_dw(const GroupedArgs& g, void*, hipStream_t s) {
-    if (tiles_fit(g)) launch_grouped_tiles_dw(g, s);
+size_t grouped_dw_workspace(const GroupedArgs& g) {
+    const int splits = chunked(g) && g.R > 0 ? grouped_tiles_dw_splits(g) : 1;
+    return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;
+}
+void launch_grouped_dw(const GroupedArgs& call, void* workspace, hipStream_t s) {
+    GroupedArgs g = call;
+    g.splits = chunked(g) && g.R > 0 ? grouped_tiles_dw_splits(g) : 1;
+    if (chunked(g)) launch_grouped_tiles_dw(g, workspace, s);
     else launch_small<kOpDw>(g, s);
 }
 

@@ -175,6 +175,7 @@ struct GroupedArgs {
     uint32_t slots, magic;       // slots = T*topk; magic of grouped_token
     int T, R, E, K, N;
     int out_f32, accumulate;
+    int splits;                  // dw on full tiles: ranges of an expert's rows
     void* out;
 };
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);
@@ -182,7 +183,8 @@ void launch_grouped_dx(const GroupedArgs& g, hipStream_t s);
 // full 256 x 256 tiles (K and N multiples of 8)
 void launch_grouped_tiles_fwd(const GroupedArgs& g, hipStream_t s);
 void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s);
-void launch_grouped_tiles_dw(const GroupedArgs& g, hipStream_t s);
+int grouped_tiles_dw_splits(const GroupedArgs& g);
+void launch_grouped_tiles_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
 size_t grouped_dw_workspace(const GroupedArgs& g);
 void launch_grouped_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
 

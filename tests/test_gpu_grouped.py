@@ -46,6 +46,12 @@ SHAPES = [
     (777, 2, 6, 192, 320, 128, (2,)),        # long, padded
     (1500, 2, 5, 640, 512, 1, (3,)),         # full tiles
     (1100, 1, 1, 1032, 776, 1, ()),          # one expert, widths that fill no tile
+    (2100, 1, 2, 72, 136, 1, ()),            # few outputs, many rows: dw in ranges
+    (3000, 1, 3, 264, 520, 1, (1,)),
+    (1500, 2, 2, 136, 72, 64, ()),
+    (4200, 1, 1, 8, 16, 1, ()),
+    (40, 2, 4, 2056, 4104, 1, ()),           # few rows, wide: small tiles
+    (9, 2, 16, 2048, 8200, 1, (3,)),
 ]
 
 

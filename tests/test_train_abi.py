@@ -63,6 +63,13 @@ def test_grouped_dw_refusals(lib):
         need = n.value
         assert need >= 256                                        # never NULL-sized
         assert call(rows=rows, nbytes=need - 1) == WSP
+    # few output tiles over many rows: fp32 products of the rows' ranges
+    assert call(None, None, None, None, 0, R=4096, E=1, dw=None, ws=None) == OK
+    assert n.value == 8 * 96 * 64 * 4
+    assert call(None, None, None, None, 0, R=4096, E=1, N=28672, K=4096, dw=None, ws=None) == OK
+    assert n.value == 256
+    assert call(None, None, None, None, 0, R=4096, E=1, N=97, dw=None, ws=None) == OK
+    assert n.value == 256
     assert call(R=0, out=2, dy=None, x=None, ids=None, rows=0) == OK     # nothing to add
 
 
