@@ -271,8 +271,17 @@ static bool full_tiles(const GroupedArgs& g, int cols) {
     return (long)((cols + kSim - 1) / kSim) * (blocks > experts ? blocks : experts) > 512;
 }
 
+// The weight stream while an expert has up to three rows on average; us, stream
+// / best of the tiles: 1x2/16 16384x4096 49/57, 8x2/8 28672x4096 286/317,
+// 16x8/64 1024x2048 44/59; at four rows 16x2/8 28672x4096 317/324 and 128x8/256
+// 7168x2048 1277/1257, at eight 32x2/8 28672x4096 339/324.
+static bool stream(const GroupedArgs& g) {
+    return chunked(g) && g.R <= 3L * (g.R < g.E ? g.R : g.E);
+}
+
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
-    if (full_tiles(g, g.N)) launch_grouped_tiles_fwd(g, s);
+    if (stream(g)) launch_grouped_stream_fwd(g, s);
+    else if (full_tiles(g, g.N)) launch_grouped_tiles_fwd(g, s);
     else launch_small<kOpFwd>(g, s);
 }
 void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {

@@ -180,6 +180,8 @@ struct GroupedArgs {
 };
 void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);
 void launch_grouped_dx(const GroupedArgs& g, hipStream_t s);
+// very few rows an expert (K and N multiples of 8)
+void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s);
 // full 256 x 256 tiles (K and N multiples of 8)
 void launch_grouped_tiles_fwd(const GroupedArgs& g, hipStream_t s);
 void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s);

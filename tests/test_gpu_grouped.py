@@ -52,6 +52,8 @@ SHAPES = [
     (4200, 1, 1, 8, 16, 1, ()),
     (40, 2, 4, 2056, 4104, 1, ()),           # few rows, wide: small tiles
     (9, 2, 16, 2048, 8200, 1, (3,)),
+    (20, 2, 16, 200, 40, 4, ()),             # the weight stream, padded, a reduction tail
+    (23, 1, 23, 4096, 24, 1, (0, 22)),
 ]
 
 
