@@ -135,9 +135,16 @@ __global__ __launch_bounds__(256, 4) void grouped_small_kernel(GroupedArgs g) {
         for (int h = 0; h < 2; ++h) {
             const int i = r + 32 * h;
             if constexpr (OP == kOpDw) {
-                const bool ok = r0 + i < red;
-                const int rx = ok ? grouped_row(g, row0 + r0 + i, g.how_x) : -1;
-                const int ry = ok ? grouped_row(g, row0 + r0 + i, g.how_dy) : -1;
+                int rx = -1, ry = -1;
+                if (r0 + i < red) {
+                    rx = ry = row0 + r0 + i;
+                    if (g.sorted) {  // one slot for both operands' rows
+                        const uint32_t p = (uint32_t)g.sorted[rx];
+                        const int t = (int)grouped_token(p, g.magic);
+                        rx = p >= g.slots ? -1 : g.how_x == kRowToken ? t : rx;
+                        ry = p >= g.slots ? -1 : g.how_dy == kRowToken ? t : ry;
+                    }
+                }
                 s.a[h] = load_chunk(rx < 0 ? nullptr : g.x + (size_t)rx * g.K, a0 + c * 8, g.K);
                 s.b[h] = load_chunk(ry < 0 ? nullptr : g.dy + (size_t)ry * g.N, b0 + c * 8, g.N);
             } else {
@@ -264,7 +271,6 @@ static bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0;
 //   dx  N x K  8x2/8 28672x4096 [512] 349/409;  128x2/8 14336x4096 [512] 199/214;
 //              256x2/8 14336x4096 [512] 253/237;  2048x2/8 1024x256 [256] 15.3/23.6;
 //              2048x2/8 2048x1024 [1024] 52.4/40.6;  8192x2/8 512x256 [1024] 19.4/17.0
-// (the weight gradient: full tiles are at least as fast throughout).
 static bool full_tiles(const GroupedArgs& g, int cols) {
     if (!chunked(g)) return false;
     const long experts = g.R < g.E ? g.R : g.E, blocks = g.R / kSim;
@@ -288,15 +294,25 @@ void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {
     if (full_tiles(g, g.K)) launch_grouped_tiles_dx(g, s);
     else launch_small<kOpDx>(g, s);
 }
+// The weight gradient on small tiles: up to four a CU, while the rows of an
+// expert are few (a full tile's start costs more than its steps there).  Kernel
+// us, small / full tiles, rows over E experts of N x K (small tiles): 666/8
+// 1032x256 [544] 9.4/15.6, 666/8 1032x512 [1088] 11.2/14.6, 2000/8 1024x256
+// [512] 17.4/24.2, 300/2 1024x1024 [512] 9.3/15.6, 1024/8 2048x1024 [4096] 34/16.
+static bool small_dw(const GroupedArgs& g) {
+    if (!chunked(g)) return true;
+    const long tiles = (long)((g.K + kSim - 1) / kSim) * ((g.N + kSim - 1) / kSim) * g.E;
+    return tiles <= 1088 && g.R <= 256L * (g.R < g.E ? g.R : g.E);
+}
 size_t grouped_dw_workspace(const GroupedArgs& g) {
-    const int splits = chunked(g) && g.R > 0 ? grouped_tiles_dw_splits(g) : 1;
+    const int splits = small_dw(g) || g.R == 0 ? 1 : grouped_tiles_dw_splits(g);
     return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;
 }
 void launch_grouped_dw(const GroupedArgs& call, void* workspace, hipStream_t s) {
     GroupedArgs g = call;
-    g.splits = chunked(g) && g.R > 0 ? grouped_tiles_dw_splits(g) : 1;
-    if (chunked(g)) launch_grouped_tiles_dw(g, workspace, s);
-    else launch_small<kOpDw>(g, s);
+    g.splits = small_dw(g) || g.R == 0 ? 1 : grouped_tiles_dw_splits(g);
+    if (small_dw(g)) launch_small<kOpDw>(g, s);
+    else launch_grouped_tiles_dw(g, workspace, s);
 }
 
 }  // namespace moe
