@@ -159,6 +159,8 @@ static moe_status gated_check(moe::GatedArgs* a, const void* g, const float* top
                               int N) {
     if (slots < 0 || R < 0 || N < 1) return MOE_ERR_INVALID_ARG;
     if (R >= kMaxRows || slots >= kMaxRows || N >= kMaxWidth) return MOE_ERR_UNSUPPORTED;
+    // a thread per 8 values, 256 a workgroup, in a one-dimensional grid
+    if ((long)R * ((N + 7) / 8) >= 256L << 31) return MOE_ERR_UNSUPPORTED;
     // without sorted_ids row i is slot i
     if (topk_weights && !sorted_ids && slots < R) return MOE_ERR_INVALID_ARG;
     if (misaligned(g) || misaligned(topk_weights) || misaligned(sorted_ids) ||

@@ -22,6 +22,7 @@
 // not depend on the order in which workgroups run.
 #include "common.hpp"
 #include "launch.hpp"
+#include "rows.hpp"
 
 #include <type_traits>
 
@@ -29,80 +30,35 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormMaxParts = 512;  // workgroups of the backward = partial rows
+constexpr int kNormThreads = 256 * 1024;  // of the backward's launch
 
-template <int V> struct Bits { typedef uint16_t type __attribute__((ext_vector_type(V))); };
-template <> struct Bits<1> { typedef uint16_t type; };
-template <int V> struct Fp { typedef float type __attribute__((ext_vector_type(V))); };
-template <> struct Fp<1> { typedef float type; };
-
-template <int V>
-__device__ __forceinline__ void ld_bf16(const uint16_t* p, float (&f)[V]) {
-    const typename Bits<V>::type v = *reinterpret_cast<const typename Bits<V>::type*>(p);
-    if constexpr (V == 1) f[0] = bf16_bits_to_f32(v);
-    else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = bf16_bits_to_f32(v[i]);
-    }
-}
-template <int V>
-__device__ __forceinline__ void st_bf16(uint16_t* p, const float (&f)[V]) {
-    if constexpr (V == 1) *p = f32_to_bf16_bits(f[0]);
-    else {
-        typename Bits<V>::type v;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = f32_to_bf16_bits(f[i]);
-        *reinterpret_cast<typename Bits<V>::type*>(p) = v;
-    }
-}
-template <int V>
-__device__ __forceinline__ void ld_f32(const float* p, float (&f)[V]) {
-    if constexpr (V == 1) f[0] = *p;
-    else {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[i + j] = v[j];
-        }
-    }
-}
-template <int V>
-__device__ __forceinline__ void st_f32(float* p, const float (&f)[V]) {
-    if constexpr (V == 1) *p = f[0];
-    else {
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<f32x4_t*>(p + i) = f32x4_t{f[i], f[i + 1], f[i + 2], f[i + 3]};
-    }
-}
 // the residual stream's type
-template <int V, bool F32>
-__device__ __forceinline__ void ld_h(const void* p, size_t at, float (&f)[V]) {
-    if constexpr (F32) ld_f32<V>((const float*)p + at, f);
-    else ld_bf16<V>((const uint16_t*)p + at, f);
+template <bool F32, bool ANY>
+__device__ __forceinline__ void ld_h(const void* p, size_t at, int n, float (&f)[V]) {
+    if constexpr (F32) ld_f32<ANY>((const float*)p + at, n, f);
+    else ld_bf16<ANY>((const uint16_t*)p + at, n, f);
 }
 // stores f and leaves in it the value as stored
-template <int V, bool F32>
-__device__ __forceinline__ void st_h(void* p, size_t at, float (&f)[V]) {
+template <bool F32, bool ANY>
+__device__ __forceinline__ void st_h(void* p, size_t at, int n, float (&f)[V]) {
     if constexpr (F32) {
-        st_f32<V>((float*)p + at, f);
+        st_f32<ANY>((float*)p + at, n, f);
     } else {
-        st_bf16<V>((uint16_t*)p + at, f);
+        st_bf16<ANY>((uint16_t*)p + at, n, f);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = bf16_bits_to_f32(f32_to_bf16_bits(f[i]));
     }
 }
 
 // sum of a token's rows t*slots .. +slots at one column group
-template <int V>
-__device__ __forceinline__ void ld_slots(const uint16_t* p, int t, int slots, int K, int col,
+template <bool ANY>
+__device__ __forceinline__ void ld_slots(const uint16_t* p, int t, int slots, int K, int col, int n,
                                          float (&f)[V]) {
     const uint16_t* q = p + (size_t)t * slots * K + col;
-    ld_bf16<V>(q, f);
+    ld_bf16<ANY>(q, n, f);
     for (int j = 1; j < slots; ++j) {
         float x[V];
-        ld_bf16<V>(q + (size_t)j * K, x);
+        ld_bf16<ANY>(q + (size_t)j * K, n, x);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] += x[i];
     }
@@ -127,7 +83,7 @@ __device__ __forceinline__ float block_sum(float v, float (&part)[2][16], int& h
 
 // C > 0: a thread keeps its C groups of V columns in registers (K <= TH*V*C);
 // C == 0: rows of any length, re-read between the passes.
-template <int TH, int V, int C, bool F32>
+template <int TH, int C, bool F32, bool ANY>
 __global__ __launch_bounds__(TH) void block_norm_kernel(NormArgs a) {
     __shared__ float part[2][16];
     int half = 0;
@@ -143,10 +99,10 @@ __global__ __launch_bounds__(TH) void block_norm_kernel(NormArgs a) {
     if (a.o) {
         float ss = 0.0f;
         for (int c = 0; c < groups; ++c) {
-            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
             if (col < a.K) {
-                if constexpr (C > 0) ld_h<V, F32>(a.h, row + col, hh[ci]);
-                ld_slots<V>(a.o, t, a.topk, a.K, col, f[ci]);
+                if constexpr (C > 0) ld_h<F32, ANY>(a.h, row + col, n, hh[ci]);
+                ld_slots<ANY>(a.o, t, a.topk, a.K, col, n, f[ci]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) ss += f[ci][i] * f[ci][i];
             }
@@ -158,17 +114,17 @@ __global__ __launch_bounds__(TH) void block_norm_kernel(NormArgs a) {
     }
     float ss = 0.0f;
     for (int c = 0; c < groups; ++c) {
-        const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+        const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
         if (col >= a.K) continue;
-        if (C == 0 || !a.o) ld_h<V, F32>(a.h, row + col, hh[ci]);
+        if (C == 0 || !a.o) ld_h<F32, ANY>(a.h, row + col, n, hh[ci]);
         if (a.o) {
-            if constexpr (C == 0) ld_slots<V>(a.o, t, a.topk, a.K, col, f[ci]);
+            if constexpr (C == 0) ld_slots<ANY>(a.o, t, a.topk, a.K, col, n, f[ci]);
             float w[V];
-            if (a.w_post) ld_f32<V>(a.w_post + col, w);
+            if (a.w_post) ld_f32<ANY>(a.w_post + col, n, w);
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 hh[ci][i] += gs * (a.w_post ? f[ci][i] * r1 * w[i] : f[ci][i]);
-            st_h<V, F32>(a.h_out, row + col, hh[ci]);
+            st_h<F32, ANY>(a.h_out, row + col, n, hh[ci]);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) ss += hh[ci][i] * hh[ci][i];
@@ -177,22 +133,22 @@ __global__ __launch_bounds__(TH) void block_norm_kernel(NormArgs a) {
     const float r2 = rsqrtf(block_sum<TH>(ss, part, half) * invk + a.eps);
     if (a.rstd_pre && tid == 0) a.rstd_pre[t] = r2;
     for (int c = 0; c < groups; ++c) {
-        const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+        const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
         if (col >= a.K) continue;
         // the thread's own columns, as it stored them
-        if constexpr (C == 0) ld_h<V, F32>(a.o ? a.h_out : a.h, row + col, hh[ci]);
+        if constexpr (C == 0) ld_h<F32, ANY>(a.o ? a.h_out : a.h, row + col, n, hh[ci]);
         float w[V], u[V];
-        ld_f32<V>(a.w_pre + col, w);
+        ld_f32<ANY>(a.w_pre + col, n, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] = hh[ci][i] * r2 * w[i];
-        st_bf16<V>(a.u + row + col, u);
+        st_bf16<ANY>(a.u + row + col, n, u);
     }
 }
 
 // A workgroup takes the rows blockIdx.x, + gridDim.x, ...; partials: gridDim.x
 // rows of K sums for dw_post, then as many for dw_pre (those that are asked
 // for).
-template <int TH, int V, int C, bool F32>
+template <int TH, int C, bool F32, bool ANY>
 __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* part_post,
                                                             float* part_pre) {
     __shared__ float part[2][16];
@@ -203,12 +159,12 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
     const int groups = C > 0 ? C : (a.K + TH * V - 1) / (TH * V);
     float sum_post[CR][V] = {}, sum_pre[CR][V] = {};
     const size_t prow = (size_t)blockIdx.x * a.K;
-    auto add = [&](float* p, int col, const float (&v)[V], bool first) {
+    auto add = [&](float* p, int col, int n, const float (&v)[V], bool first) {
         float x[V];
-        if (!first) ld_f32<V>(p + prow + col, x);
+        if (!first) ld_f32<ANY>(p + prow + col, n, x);
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = first ? v[i] : x[i] + v[i];
-        st_f32<V>(p + prow + col, x);
+        st_f32<ANY>(p + prow + col, n, x);
     };
     for (int t = (int)blockIdx.x; t < a.M; t += (int)gridDim.x) {
         const bool first = t == (int)blockIdx.x;
@@ -216,65 +172,65 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
         const float gs = a.res_scale * (a.gate ? a.gate[t] : 1.0f);
         const float r1 = a.w_post ? a.rstd_post_in[t] : 1.0f;
         const float r2 = a.w_pre ? a.rstd_pre_in[t] : 1.0f;
-        float dh[CR][V], n[CR][V], z[CR][V];
+        float dh[CR][V], hn[CR][V], z[CR][V];
         float s1 = 0.0f;
         // n and dn = du w_pre (kept in dh) of one group
-        auto load_pre = [&](int ci, int col, float (&du)[V]) {
+        auto load_pre = [&](int ci, int col, int n, float (&du)[V]) {
             float w[V];
-            ld_slots<V>(a.du, t, a.du_topk, a.K, col, du);
-            ld_h<V, F32>(a.h, row + col, n[ci]);
-            ld_f32<V>(a.w_pre + col, w);
+            ld_slots<ANY>(a.du, t, a.du_topk, a.K, col, n, du);
+            ld_h<F32, ANY>(a.h, row + col, n, hn[ci]);
+            ld_f32<ANY>(a.w_pre + col, n, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                n[ci][i] *= r2;
+                hn[ci][i] *= r2;
                 dh[ci][i] = du[i] * w[i];
             }
         };
         if (a.w_pre) {
             for (int c = 0; c < groups; ++c) {
-                const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+                const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
                 if (col >= a.K) continue;
                 float du[V];
-                load_pre(ci, col, du);
+                load_pre(ci, col, n, du);
                 if constexpr (C > 0)
-                    if (a.o) ld_slots<V>(a.o, t, a.topk, a.K, col, z[ci]);
+                    if (a.o) ld_slots<ANY>(a.o, t, a.topk, a.K, col, n, z[ci]);
                 float dn[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    s1 += dh[ci][i] * n[ci][i];
-                    dn[i] = du[i] * n[ci][i];
+                    s1 += dh[ci][i] * hn[ci][i];
+                    dn[i] = du[i] * hn[ci][i];
                 }
                 if constexpr (C > 0) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) sum_pre[ci][i] += dn[i];
                 } else {
-                    add(part_pre, col, dn, first);
+                    add(part_pre, col, n, dn, first);
                 }
             }
             s1 = block_sum<TH>(s1, part, half) * invk;
         }
         float s2 = 0.0f;
         for (int c = 0; c < groups; ++c) {
-            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
             if (col >= a.K) continue;
             float g[V] = {};
-            if (a.dh_out) ld_h<V, F32>(a.dh_out, row + col, g);
+            if (a.dh_out) ld_h<F32, ANY>(a.dh_out, row + col, n, g);
             if (a.w_pre) {
                 if constexpr (C == 0) {
                     float du[V];
-                    load_pre(ci, col, du);
+                    load_pre(ci, col, n, du);
                 }
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] += r2 * (dh[ci][i] - n[ci][i] * s1);
+                for (int i = 0; i < V; ++i) g[i] += r2 * (dh[ci][i] - hn[ci][i] * s1);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) dh[ci][i] = g[i];
-            if constexpr (F32) st_f32<V>((float*)a.h_out + row + col, g);
-            else st_bf16<V>((uint16_t*)a.h_out + row + col, g);
+            if constexpr (F32) st_f32<ANY>((float*)a.h_out + row + col, n, g);
+            else st_bf16<ANY>((uint16_t*)a.h_out + row + col, n, g);
             if (!a.o) continue;
-            if (C == 0 || !a.w_pre) ld_slots<V>(a.o, t, a.topk, a.K, col, z[ci]);
+            if (C == 0 || !a.w_pre) ld_slots<ANY>(a.o, t, a.topk, a.K, col, n, z[ci]);
             float w[V], dz[V];
-            if (a.w_post) ld_f32<V>(a.w_post + col, w);
+            if (a.w_post) ld_f32<ANY>(a.w_post + col, n, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 z[ci][i] *= r1;
@@ -287,7 +243,7 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
 #pragma unroll
                 for (int i = 0; i < V; ++i) sum_post[ci][i] += dz[i];
             } else {
-                add(part_post, col, dz, first);
+                add(part_post, col, n, dz, first);
             }
         }
         if (!a.o) continue;
@@ -295,20 +251,20 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
         if (a.dgate && tid == 0) a.dgate[t] = a.res_scale * s2;
         s2 *= invk;
         for (int c = 0; c < groups; ++c) {
-            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0;
+            const int col = (c * TH + tid) * V, ci = C > 0 ? c : 0, n = ANY ? min(V, a.K - col) : V;
             if (col >= a.K) continue;
             if constexpr (C == 0) {
                 // b and z again: dh from its inputs, not from its rounding
                 float g[V] = {}, w[V];
-                if (a.dh_out) ld_h<V, F32>(a.dh_out, row + col, g);
+                if (a.dh_out) ld_h<F32, ANY>(a.dh_out, row + col, n, g);
                 if (a.w_pre) {
                     float du[V];
-                    load_pre(ci, col, du);
+                    load_pre(ci, col, n, du);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) g[i] += r2 * (dh[ci][i] - n[ci][i] * s1);
+                    for (int i = 0; i < V; ++i) g[i] += r2 * (dh[ci][i] - hn[ci][i] * s1);
                 }
-                ld_slots<V>(a.o, t, a.topk, a.K, col, z[ci]);
-                if (a.w_post) ld_f32<V>(a.w_post + col, w);
+                ld_slots<ANY>(a.o, t, a.topk, a.K, col, n, z[ci]);
+                if (a.w_post) ld_f32<ANY>(a.w_post + col, n, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     z[ci][i] *= r1;
@@ -319,22 +275,22 @@ __global__ __launch_bounds__(TH) void block_norm_bwd_kernel(NormArgs a, float* p
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 y[i] = gs * (a.w_post ? r1 * (dh[ci][i] - z[ci][i] * s2) : dh[ci][i]);
-            st_bf16<V>(a.u + row + col, y);
+            st_bf16<ANY>(a.u + row + col, n, y);
         }
     }
     if constexpr (C > 0) {
         for (int c = 0; c < groups; ++c) {
-            const int col = (c * TH + tid) * V;
+            const int col = (c * TH + tid) * V, n = ANY ? min(V, a.K - col) : V;
             if (col >= a.K) continue;
-            if (part_post) st_f32<V>(part_post + prow + col, sum_post[c]);
-            if (part_pre) st_f32<V>(part_pre + prow + col, sum_pre[c]);
+            if (part_post) st_f32<ANY>(part_post + prow + col, n, sum_post[c]);
+            if (part_pre) st_f32<ANY>(part_pre + prow + col, n, sum_pre[c]);
         }
     }
 }
 
-// dw[k] = sum of the partial rows: 32 columns a workgroup, 16 threads a column
-// each adding every 16th row in ascending order, then the 16 sums in order
-constexpr int kPartCols = 32, kPartRows = 16;
+// dw[k] = sum of the partial rows: 32 columns a workgroup, 32 threads a column
+// each adding every 32nd row in ascending order, then the 32 sums in order
+constexpr int kPartCols = 32, kPartRows = 32;
 __global__ __launch_bounds__(kPartCols * kPartRows) void norm_parts_kernel(
     const float* post, const float* pre, int parts, int K, float* dw_post, float* dw_pre) {
     __shared__ float sums[kPartRows][kPartCols];
@@ -364,49 +320,79 @@ __global__ __launch_bounds__(kPartCols * kPartRows) void norm_parts_kernel(
     }
 }
 
-// Threads, columns per load and column groups that hold a row of K columns in
-// registers; rows that are no multiple of 8 long, or too long, are re-read.
-template <int TH, int V, int C>
+// Threads and column groups that hold a row of K columns in registers; longer
+// rows are re-read.
+// The backward holds five rows of values and two of sums: one group a thread
+// (126 registers, four waves a SIMD) took 74 us where two groups with half the
+// threads (194 registers, two waves) took 87 (4096 rows of 4096, two slots,
+// fp32 stream: 385 MB).
+template <int TH, int C>
 struct Shape {
-    static constexpr int kThreads = TH, kVec = V, kGroups = C;
+    static constexpr int kThreads = TH, kGroups = C;
 };
 template <bool BWD, typename F>
 void pick_shape(int K, const F& f) {
-    if (K % 8 || K > 16384) f(Shape<256, 1, 0>{});
-    else if (K <= 512) f(Shape<64, 8, 1>{});
-    else if (K <= 2048) f(Shape<256, 8, 1>{});
-    else if (K <= 4096) f(Shape<256, 8, 2>{});
-    else if (K <= 8192) f(Shape<512, 8, 2>{});
-    // the backward's five rows of values fit 512 threads' registers, not 1024's
-    else if constexpr (BWD) f(Shape<512, 8, 4>{});
-    else f(Shape<1024, 8, 2>{});
+    if (K <= 512) return f(Shape<64, 1>{});
+    if (K <= 1024) return f(Shape<128, 1>{});
+    if (K <= 2048) return f(Shape<256, 1>{});
+    if constexpr (BWD) {
+        if (K <= 4096) return f(Shape<512, 1>{});
+        if (K <= 8192) return f(Shape<1024, 1>{});
+    } else {
+        if (K <= 4096) return f(Shape<256, 2>{});
+        if (K <= 8192) return f(Shape<512, 2>{});
+        if (K <= 16384) return f(Shape<1024, 2>{});
+    }
+    f(Shape<512, 0>{});
 }
 
-int norm_parts(int M) { return M < kNormMaxParts ? M : kNormMaxParts; }
+template <typename F>
+void with_types(const NormArgs& a, const F& run) {
+    if (a.K % V == 0) {
+        if (a.h_f32) run(std::true_type{}, std::false_type{});
+        else run(std::false_type{}, std::false_type{});
+    } else {
+        if (a.h_f32) run(std::true_type{}, std::true_type{});
+        else run(std::false_type{}, std::true_type{});
+    }
+}
+
+// Workgroups of the backward, each with one partial row of either gradient:
+// 1024 threads a CU.
+int norm_parts(int M, int K) {
+    int parts = 0;
+    pick_shape<true>(K, [&](auto shape) { parts = kNormThreads / shape.kThreads; });
+    return M < parts ? M : parts;
+}
 
 }  // namespace
 
 void launch_block_norm(const NormArgs& a, hipStream_t s) {
     pick_shape<false>(a.K, [&](auto shape) {
-        constexpr int TH = shape.kThreads, V = shape.kVec, C = shape.kGroups;
-        if (a.h_f32) block_norm_kernel<TH, V, C, true><<<a.M, TH, 0, s>>>(a);
-        else block_norm_kernel<TH, V, C, false><<<a.M, TH, 0, s>>>(a);
+        constexpr int TH = shape.kThreads, C = shape.kGroups;
+        auto run = [&](auto f32, auto any) {
+            block_norm_kernel<TH, C, decltype(f32)::value, decltype(any)::value><<<a.M, TH, 0, s>>>(a);
+        };
+        with_types(a, run);
     });
 }
 
 size_t block_norm_bwd_workspace(int M, int K, bool post, bool pre) {
-    return (size_t)norm_parts(M) * K * 4 * ((post ? 1 : 0) + (pre ? 1 : 0));
+    return (size_t)norm_parts(M, K) * K * 4 * ((post ? 1 : 0) + (pre ? 1 : 0));
 }
 
 void launch_block_norm_bwd(const NormArgs& a, float* partials, hipStream_t s) {
-    const int parts = norm_parts(a.M);
+    const int parts = norm_parts(a.M, a.K);
     float* post = a.w_post ? partials : nullptr;
     float* pre = a.w_pre ? partials + (a.w_post ? (size_t)parts * a.K : 0) : nullptr;
     if (parts)
         pick_shape<true>(a.K, [&](auto shape) {
-            constexpr int TH = shape.kThreads, V = shape.kVec, C = shape.kGroups;
-            if (a.h_f32) block_norm_bwd_kernel<TH, V, C, true><<<parts, TH, 0, s>>>(a, post, pre);
-            else block_norm_bwd_kernel<TH, V, C, false><<<parts, TH, 0, s>>>(a, post, pre);
+            constexpr int TH = shape.kThreads, C = shape.kGroups;
+            auto run = [&](auto f32, auto any) {
+                block_norm_bwd_kernel<TH, C, decltype(f32)::value, decltype(any)::value>
+                    <<<parts, TH, 0, s>>>(a, post, pre);
+            };
+            with_types(a, run);
         });
     if (post || pre)
         norm_parts_kernel<<<dim3((a.K + kPartCols - 1) / kPartCols, 2), kPartCols * kPartRows, 0, s>>>(

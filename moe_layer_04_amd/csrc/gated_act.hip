@@ -7,39 +7,17 @@
 //   dw[p]   = sum_n da[i,n] silu(g[i,n]) u[i,n]
 //
 // p = sorted[i] is the row's slot.  Rows hold the gate half, then the up
-// half.  Both passes are bound by HBM: every value is read and written once,
-// a workgroup per row, 16 bytes a lane; arithmetic and the row's dot product
-// are fp32.
+// half.  Both passes are bound by HBM: every value is read and written once, 16
+// bytes a lane; arithmetic and the row's dot product are fp32.
 #include "common.hpp"
 #include "launch.hpp"
+#include "rows.hpp"
+
+#include <type_traits>
 
 namespace moe {
 
 namespace {
-
-template <int V> struct Vec16 { typedef uint16_t type __attribute__((ext_vector_type(V))); };
-template <> struct Vec16<1> { typedef uint16_t type; };
-
-template <int V>
-__device__ __forceinline__ void load_row(const uint16_t* p, float (&f)[V]) {
-    const typename Vec16<V>::type v = *reinterpret_cast<const typename Vec16<V>::type*>(p);
-    if constexpr (V == 1) f[0] = bf16_bits_to_f32(v);
-    else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = bf16_bits_to_f32(v[i]);
-    }
-}
-
-template <int V>
-__device__ __forceinline__ void store_row(uint16_t* p, const float (&f)[V]) {
-    if constexpr (V == 1) *p = f32_to_bf16_bits(f[0]);
-    else {
-        typename Vec16<V>::type v;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = f32_to_bf16_bits(f[i]);
-        *reinterpret_cast<typename Vec16<V>::type*>(p) = v;
-    }
-}
 
 // slot of row i: -1 padding, -2 a row past *num_rows (not touched)
 __device__ __forceinline__ int gated_slot(const GatedArgs& a, int i) {
@@ -49,29 +27,34 @@ __device__ __forceinline__ int gated_slot(const GatedArgs& a, int i) {
     return p < a.slots ? (int)p : -1;
 }
 
-template <int V>
+// a thread per 8 columns, rows one after the other
+template <bool ANY>
 __global__ __launch_bounds__(256) void silu_mul_kernel(GatedArgs a) {
-    const int i = (int)blockIdx.x;
-    const int p = gated_slot(a, i);
+    const uint32_t per_row = ((uint32_t)a.N + V - 1) / V;
+    const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    // (a 32-bit division while the index fits)
+    const uint32_t i = at >> 32 ? (uint32_t)(at / per_row) : (uint32_t)at / per_row;
+    if (i >= (uint32_t)a.R) return;
+    const int col = (int)(at - (uint64_t)i * per_row) * V, n = ANY ? min(V, a.N - col) : V;
+    const int p = gated_slot(a, (int)i);
     if (p == -2) return;
-    const int n = ((int)blockIdx.y * 256 + (int)threadIdx.x) * V;
-    if (n >= a.N) return;
-    const uint16_t* g = a.g + (size_t)i * 2 * a.N + n;
+    const uint16_t* g = a.g + (size_t)i * 2 * a.N + col;
     float y[V] = {};
     if (p >= 0) {
         const float w = a.weights ? a.weights[p] : 1.0f;
         float z[V], u[V];
-        load_row<V>(g, z);
-        load_row<V>(g + a.N, u);
+        ld_bf16<ANY>(g, n, z);
+        ld_bf16<ANY>(g + a.N, n, u);
 #pragma unroll
         for (int v = 0; v < V; ++v) y[v] = w * silu(z[v]) * u[v];
     }
-    store_row<V>(a.out + (size_t)i * a.N + n, y);
+    st_bf16<ANY>(a.out + (size_t)i * a.N + col, n, y);
 }
 
-template <int V>
-__global__ __launch_bounds__(256) void silu_mul_bwd_kernel(GatedArgs a) {
-    __shared__ float part[4];
+// a workgroup per row
+template <int TH, bool ANY>
+__global__ __launch_bounds__(TH) void silu_mul_bwd_kernel(GatedArgs a) {
+    __shared__ float part[TH / kWave];
     const int i = (int)blockIdx.x;
     const int p = gated_slot(a, i);
     if (p == -2) return;
@@ -80,13 +63,14 @@ __global__ __launch_bounds__(256) void silu_mul_bwd_kernel(GatedArgs a) {
     const uint16_t* d = a.da + (size_t)i * a.N;
     uint16_t* o = a.out + (size_t)i * 2 * a.N;
     float dot = 0.0f;
-    for (int n = (int)threadIdx.x * V; n < a.N; n += 256 * V) {
+    for (int col = (int)threadIdx.x * V; col < a.N; col += TH * V) {
+        const int n = ANY ? min(V, a.N - col) : V;
         float dg[V] = {}, du[V] = {};
         if (p >= 0) {
             float z[V], u[V], da[V];
-            load_row<V>(g + n, z);
-            load_row<V>(g + a.N + n, u);
-            load_row<V>(d + n, da);
+            ld_bf16<ANY>(g + col, n, z);
+            ld_bf16<ANY>(g + a.N + col, n, u);
+            ld_bf16<ANY>(d + col, n, da);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z[v]));
@@ -96,28 +80,38 @@ __global__ __launch_bounds__(256) void silu_mul_bwd_kernel(GatedArgs a) {
                 du[v] = da[v] * w * act;
             }
         }
-        store_row<V>(o + n, dg);
-        store_row<V>(o + a.N + n, du);
+        st_bf16<ANY>(o + col, n, dg);
+        st_bf16<ANY>(o + a.N + col, n, du);
     }
     if (!a.dweights || p < 0) return;  // the same for the whole workgroup
     dot = wave_sum_f32(dot);
-    if (lane_id() == 0) part[threadIdx.x / kWave] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) a.dweights[p] = (part[0] + part[1]) + (part[2] + part[3]);
+    if constexpr (TH > kWave) {
+        if (lane_id() == 0) part[threadIdx.x / kWave] = dot;
+        __syncthreads();
+        dot = part[0];
+#pragma unroll
+        for (int k = 1; k < TH / kWave; ++k) dot += part[k];
+    }
+    if (threadIdx.x == 0) a.dweights[p] = dot;
 }
 
 }  // namespace
 
 void launch_silu_mul(const GatedArgs& a, hipStream_t s) {
-    const int per = a.N % 8 == 0 ? 256 * 8 : 256;
-    const dim3 grid(a.R, (a.N + per - 1) / per);
-    if (a.N % 8 == 0) silu_mul_kernel<8><<<grid, 256, 0, s>>>(a);
-    else silu_mul_kernel<1><<<grid, 256, 0, s>>>(a);
+    const long threads = (long)a.R * ((a.N + V - 1) / V);
+    const int grid = (int)((threads + 255) / 256);
+    if (a.N % V == 0) silu_mul_kernel<false><<<grid, 256, 0, s>>>(a);
+    else silu_mul_kernel<true><<<grid, 256, 0, s>>>(a);
 }
 
 void launch_silu_mul_bwd(const GatedArgs& a, hipStream_t s) {
-    if (a.N % 8 == 0) silu_mul_bwd_kernel<8><<<a.R, 256, 0, s>>>(a);
-    else silu_mul_bwd_kernel<1><<<a.R, 256, 0, s>>>(a);
+    auto run = [&](auto any) {
+        constexpr bool ANY = decltype(any)::value;
+        if (a.N <= kWave * V) silu_mul_bwd_kernel<kWave, ANY><<<a.R, kWave, 0, s>>>(a);
+        else silu_mul_bwd_kernel<256, ANY><<<a.R, 256, 0, s>>>(a);
+    };
+    if (a.N % V == 0) run(std::false_type{});
+    else run(std::true_type{});
 }
 
 }  // namespace moe

@@ -46,17 +46,31 @@ constexpr int kSimAhead = 2;                   // steps loaded ahead
 typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
 
-// columns c..c+7 of a row of `width`; zeros past its end and for no row
+// Columns c..c+7 of a row of `width`, zeros past its end and for no row.  A
+// row's last chunk is loaded as the row's last 8 values, so that nothing past
+// the row is read, and moved into place by settle_chunk when it is stored (a
+// move here would wait for the load).
+template <bool WHOLE>  // the width is a multiple of 8
 __device__ __forceinline__ u16x8_t load_chunk(const uint16_t* row, int c, int width) {
     u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (!row) return v;
-    if (c + 8 <= width) return *reinterpret_cast<const u16x8_any_t*>(row + c);
-    if (c < width) {
+    if constexpr (WHOLE) {
+        if (row && c < width) v = *reinterpret_cast<const u16x8_t*>(row + c);
+    } else if (width < 8) {
 #pragma unroll
         for (int i = 0; i < 7; ++i)
-            if (c + i < width) v[i] = row[c + i];
+            if (row && c + i < width) v[i] = row[c + i];
+    } else if (row && c < width) {
+        v = *reinterpret_cast<const u16x8_any_t*>(row + min(c, width - 8));
     }
     return v;
+}
+__device__ __forceinline__ u16x8_t settle_chunk(u16x8_t v, int c, int width) {
+    const int by = width < 8 ? 0 : max(c - (width - 8), 0);  // elements to drop in front (0..7)
+    uint4 w = __builtin_bit_cast(uint4, v);
+    if (by & 4) w = uint4{w.z, w.w, 0, 0};
+    if (by & 2) w = uint4{w.y, w.z, w.w, 0};
+    if (by & 1) w = uint4{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
+    return __builtin_bit_cast(u16x8_t, w);
 }
 
 // chunk c (of 8) of row r, by layout
@@ -86,8 +100,8 @@ __device__ __forceinline__ bf16x8_t sim_frag(const char* buf, int first, int ks,
     }
 }
 
-template <int OP>
-__global__ __launch_bounds__(256, 4) void grouped_small_kernel(GroupedArgs g) {
+template <int OP, bool WHOLE>
+__global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel(GroupedArgs g) {
     constexpr bool ACOL = OP != kOpFwd, BCOL = OP == kOpDw;
     __shared__ __attribute__((aligned(16))) char lds[2][2 * kSimBytes];
     const int tid = (int)threadIdx.x, lane = lane_id();
@@ -145,17 +159,34 @@ __global__ __launch_bounds__(256, 4) void grouped_small_kernel(GroupedArgs g) {
                         ry = p >= g.slots ? -1 : g.how_dy == kRowToken ? t : ry;
                     }
                 }
-                s.a[h] = load_chunk(rx < 0 ? nullptr : g.x + (size_t)rx * g.K, a0 + c * 8, g.K);
-                s.b[h] = load_chunk(ry < 0 ? nullptr : g.dy + (size_t)ry * g.N, b0 + c * 8, g.N);
+                s.a[h] = load_chunk<WHOLE>(rx < 0 ? nullptr : g.x + (size_t)rx * g.K, a0 + c * 8, g.K);
+                s.b[h] = load_chunk<WHOLE>(ry < 0 ? nullptr : g.dy + (size_t)ry * g.N, b0 + c * 8, g.N);
             } else {
                 if constexpr (OP == kOpFwd)
-                    s.a[h] = load_chunk(a0 + i < g.N ? w + (size_t)(a0 + i) * g.K : nullptr, r0 + c * 8, red);
+                    s.a[h] = load_chunk<WHOLE>(a0 + i < g.N ? w + (size_t)(a0 + i) * g.K : nullptr, r0 + c * 8, red);
                 else
-                    s.a[h] = load_chunk(r0 + i < red ? w + (size_t)(r0 + i) * g.K : nullptr, a0 + c * 8, g.K);
-                s.b[h] = load_chunk(brow[h], r0 + c * 8, red);
+                    s.a[h] = load_chunk<WHOLE>(r0 + i < red ? w + (size_t)(r0 + i) * g.K : nullptr, a0 + c * 8, g.K);
+                s.b[h] = load_chunk<WHOLE>(brow[h], r0 + c * 8, red);
             }
         }
         return s;
+    };
+    // whether a step has chunks to settle: last columns of the tile, or the end
+    // of a reduction that runs along the rows
+    const bool a_ends = ACOL && a0 + kSim > g.K, b_ends = BCOL && b0 + kSim > g.N;
+    auto settle = [&](Step& s, int step) {
+        if constexpr (WHOLE) return;
+        const int r0 = step * kSim;
+        if (a_ends || (!ACOL && r0 + kSim > red)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                s.a[h] = settle_chunk(s.a[h], (ACOL ? a0 : r0) + c * 8, ACOL ? g.K : red);
+        }
+        if (b_ends || (!BCOL && r0 + kSim > red)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                s.b[h] = settle_chunk(s.b[h], (BCOL ? b0 : r0) + c * 8, BCOL ? g.N : red);
+        }
     };
     const int fa0 = (wave & 1) * 32, fb0 = (wave >> 1) * 32;
     f32x4_t acc[2][2];
@@ -174,6 +205,7 @@ __global__ __launch_bounds__(256, 4) void grouped_small_kernel(GroupedArgs g) {
             const int s = s0 + i;
             if (s >= steps) break;
             char* buf = lds[s & 1];
+            settle(ahead[i], s);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 *reinterpret_cast<u16x8_t*>(buf + sim_at<ACOL>(r + 32 * h, c)) = ahead[i].a[h];
@@ -250,17 +282,18 @@ int blocks_bound(const GroupedArgs& g, int B) {
     return g.R / B + (g.R < g.E ? g.R : g.E);
 }
 
+// every row of an operand is whole 16-byte chunks
+bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
+
 template <int OP>
 void launch_small(const GroupedArgs& g, hipStream_t s) {
     const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + kSim - 1) / kSim;
     const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSim - 1) / kSim) : blocks_bound(g, kSim);
-    grouped_small_kernel<OP><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+    if (chunked(g)) grouped_small_kernel<OP, true><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+    else grouped_small_kernel<OP, false><<<a_tiles * b_tiles, 256, 0, s>>>(g);
 }
 
 }  // namespace
-
-// full tiles: every row of an operand is whole 16-byte chunks
-static bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
 
 // Row products on full tiles, one a CU, unless the small tiles are few: up to
 // two a CU their shorter step wins (about 0.6-1 us against 1.3-1.5 us), beyond

@@ -121,7 +121,8 @@ def test_silu_refusals(moe):
 # M, K, topk, du_topk
 NORM = [(1, 1, 1, 1), (1, 64, 2, 2), (2, 100, 3, 1), (3, 512, 1, 4), (5, 520, 2, 2),
         (8, 4096, 2, 2), (4, 2048, 8, 8), (7, 7168, 8, 1), (3, 8200, 2, 2), (2, 16384, 2, 2),
-        (2, 16392, 1, 2), (3, 333, 2, 2), (1030, 72, 2, 2), (600, 1032, 1, 1), (2, 20001, 2, 1)]
+        (2, 16392, 1, 2), (3, 333, 2, 2), (1030, 72, 2, 2), (600, 1032, 1, 1), (2, 20001, 2, 1),
+        (4, 1000, 1, 1), (3, 3000, 2, 2), (520, 4096, 1, 2), (2, 6008, 3, 1), (1, 40960, 2, 2)]
 PARTS = ["all", "no_gate", "no_post", "pre_only", "no_pre", "add"]
 
 
