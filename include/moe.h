@@ -449,8 +449,10 @@ typedef enum {
  *                   Without SCATTER a padding row inside a range is written
  *                   as zeros.
  *   out, dw         moe_out; out [E,N,K] bf16 or fp32
- *   workspace       as moe_align_ex (moe_grouped_gemm_dw); the size depends on
- *                   (rows, T, topk, R, E, K, N, out) only
+ *   workspace       as moe_align_ex; the size depends on (rows, T, topk, R, E,
+ *                   K, N) and, for dw, out only; 256: it is not used
+ *
+ * y, dx and dw must not overlap an operand.
  *
  * Results do not depend on scheduling: every sum has a fixed order.  R == 0
  * is a no-op for y and dx; dw is written (or left, FP32_ADD).
@@ -463,10 +465,12 @@ typedef enum {
  */
 moe_status moe_grouped_gemm(const void *x, const void *w, const int32_t *expert_offsets,
                             const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
-                            int K, int N, void *y, void *stream);
+                            int K, int N, void *y, void *workspace, size_t *workspace_bytes,
+                            void *stream);
 moe_status moe_grouped_gemm_dx(const void *dy, const void *w, const int32_t *expert_offsets,
                                const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
-                               int K, int N, void *dx, void *stream);
+                               int K, int N, void *dx, void *workspace, size_t *workspace_bytes,
+                               void *stream);
 moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *expert_offsets,
                                const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
                                int K, int N, int out, void *dw, void *workspace,

@@ -96,8 +96,8 @@ def load_library(build_if_missing: bool = False):
         lib.moe_fused_graph_launch.argtypes = [P, P]
         lib.moe_fused_graph_destroy.argtypes = [P]
         F = ctypes.c_float
-        lib.moe_grouped_gemm.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P]
-        lib.moe_grouped_gemm_dx.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P]
+        lib.moe_grouped_gemm.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, SZP, P]
+        lib.moe_grouped_gemm_dx.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, SZP, P]
         lib.moe_grouped_gemm_dw.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, SZP, P]
         lib.moe_silu_mul.argtypes = [P, P, P, P, I, I, I, P, P]
         lib.moe_silu_mul_bwd.argtypes = [P, P, P, P, P, I, I, I, P, P, P]

@@ -24,6 +24,8 @@ MOE_OUT_BF16 = 0
 MOE_OUT_FP32 = 1
 MOE_OUT_FP32_ADD = 2
 
+_UNUSED = 256  # workspace bytes of a product that needs none
+
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
@@ -79,9 +81,18 @@ def _out(out, name: str, dtype, shape, device):
     return _arg(out, name, dtype, shape, device)
 
 
-def _workspace(device, workspace, nbytes: int):
-    """The caller's workspace, or one allocated here; the library checks the size."""
+@functools.lru_cache(maxsize=None)
+def _unused(device) -> torch.Tensor:
+    return torch.empty(_UNUSED, dtype=torch.uint8, device=device)
+
+
+def _workspace(device, workspace, nbytes: int, product: bool = False):
+    """The caller's workspace, or one allocated here; the library checks the
+    size.  A product that reports the least size does not touch it: one buffer
+    serves all of them."""
     if workspace is None:
+        if product and nbytes == _UNUSED:
+            return _unused(device)
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
     if workspace.numel() < nbytes:  # an empty one's null pointer would ask for the size
@@ -89,12 +100,11 @@ def _workspace(device, workspace, nbytes: int):
     return workspace
 
 
-@functools.lru_cache(maxsize=256)
-def _dw_workspace(*sizes) -> int:
+@functools.lru_cache(maxsize=1024)
+def _product_workspace(name: str, *sizes) -> int:
     nbytes = ctypes.c_size_t(0)
-    _check(_fn("moe_grouped_gemm_dw")(None, None, None, None, *sizes, None, None,
-                                      ctypes.byref(nbytes), None),
-           "moe_grouped_gemm_dw (size query)")
+    _check(_fn(name)(None, None, None, None, *sizes, None, None, ctypes.byref(nbytes), None),
+           f"{name} (size query)")
     return nbytes.value
 
 
@@ -127,7 +137,7 @@ def _rows(sorted_ids, expert_offsets, num_tokens, gather_from, any_rows: bool, E
 
 
 def _product(name, rows_in, w, expert_offsets, sorted_ids, topk, num_tokens, gather, scatter, out,
-             dx: bool):
+             workspace, dx: bool):
     E, N, K = _sizes(w, "w", 3)
     dev = w.device
     _arg(w, "w", _BF16, (E, N, K), dev)
@@ -140,15 +150,19 @@ def _product(name, rows_in, w, expert_offsets, sorted_ids, topk, num_tokens, gat
         raise ValueError(f"the operand has {count} rows, sorted_ids {R}")
     out = _out(out, "out", _BF16, (T * topk if scatter else R, K if dx else N), dev)
     rows = (MOE_ROWS_GATHER if gather else 0) | (MOE_ROWS_SCATTER if scatter else 0)
-    _call(dev, name, _p(rows_in), _p(w), _p(expert_offsets), _p(sorted_ids), rows, T, topk, R, E,
-          K, N, _p(out))
+    sizes = (rows, T, topk, R, E, K, N)
+    workspace = _workspace(dev, workspace, _product_workspace(name, *sizes), True)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    _call(dev, name, _p(rows_in), _p(w), _p(expert_offsets), _p(sorted_ids), *sizes, _p(out),
+          _p(workspace), ctypes.byref(nbytes))
     return out
 
 
 def moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor, *,
                      sorted_ids: Optional[torch.Tensor] = None, topk: int = 1,
                      num_tokens: Optional[int] = None, gather: bool = False,
-                     scatter: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     scatter: bool = False, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[i] = w[e] x[i] for the sorted rows i of every expert e's range
     (expert_offsets, sorted_ids: moe_align's).
 
@@ -157,19 +171,19 @@ def moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Ten
     [num_tokens*topk,N] in slot order.  Rows of a new output that no sorted
     row writes are uninitialised."""
     return _product("moe_grouped_gemm", x, w, expert_offsets, sorted_ids, topk, num_tokens, gather,
-                    scatter, out, False)
+                    scatter, out, workspace, False)
 
 
 def moe_grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor, *,
                         sorted_ids: Optional[torch.Tensor] = None, topk: int = 1,
                         num_tokens: Optional[int] = None, gather: bool = False,
-                        scatter: bool = False,
-                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                        scatter: bool = False, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx[i] = w[e]^T dy[i]: the gradient of moe_grouped_gemm's input rows.
     dy bf16 [R,N] (or [num_tokens,N] with ``gather``); returns bf16 [R,K], or
     [num_tokens*topk,K] with ``scatter``."""
     return _product("moe_grouped_gemm_dx", dy, w, expert_offsets, sorted_ids, topk, num_tokens,
-                    gather, scatter, out, True)
+                    gather, scatter, out, workspace, True)
 
 
 def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor, *,
@@ -206,7 +220,7 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype is _F32 else MOE_OUT_BF16
     rows = (MOE_ROWS_GATHER if gather_x else 0) | (MOE_ROWS_GATHER_DY if gather_dy else 0)
     sizes = (rows, T, topk, R, E, K, N, mode)
-    workspace = _workspace(dev, workspace, _dw_workspace(*sizes))
+    workspace = _workspace(dev, workspace, _product_workspace("moe_grouped_gemm_dw", *sizes), True)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, "moe_grouped_gemm_dw", _p(dy), _p(x), _p(expert_offsets), _p(sorted_ids), *sizes,
           _p(out), _p(workspace), ctypes.byref(nbytes))

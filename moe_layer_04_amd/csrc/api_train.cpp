@@ -36,6 +36,12 @@ bool workspace_step(void* workspace, size_t* bytes, size_t need, moe_status* st)
     return true;
 }
 
+// The size a product reports: the minimum exactly if it does not use it, so
+// that a caller may pass any buffer then.
+size_t product_size(size_t need) {
+    return need == 0 ? 0 : need < 2 * kAlign ? 2 * kAlign : round_up(need);
+}
+
 // The checks that the three products share; fills g.  `flags`: the moe_rows
 // bits the product knows.
 moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int32_t* sorted_ids,
@@ -71,13 +77,17 @@ moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int3
 // fwd (dx false) and dx
 moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
                         const int32_t* sorted_ids, int rows, int T, int topk, int R, int E, int K,
-                        int N, void* out, void* stream) {
+                        int N, void* out, void* workspace, size_t* workspace_bytes, void* stream) {
+    if (!workspace_bytes) return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g;
-    const moe_status st = grouped_setup(&g, offsets, sorted_ids, rows,
-                                        MOE_ROWS_GATHER | MOE_ROWS_SCATTER, T, topk, R, E, K, N);
+    // the size query has no pointers
+    moe_status st = grouped_setup(&g, offsets, workspace ? sorted_ids : (const int32_t*)kAlign, rows,
+                                  MOE_ROWS_GATHER | MOE_ROWS_SCATTER, T, topk, R, E, K, N);
     if (st != MOE_OK) return st;
     if ((rows & MOE_ROWS_GATHER) && (long)T * (dx ? N : K) * 2 >= kMaxGather)
         return MOE_ERR_UNSUPPORTED;
+    const size_t need = dx ? moe::grouped_dx_workspace(g) : moe::grouped_fwd_workspace(g);
+    if (workspace_step(workspace, workspace_bytes, product_size(need), &st)) return st;
     if (R == 0) return MOE_OK;
     // with T == 0 every row is padding, and a gathered / scattered operand has no rows
     if ((!in && !(T == 0 && (rows & MOE_ROWS_GATHER))) || !w || !offsets ||
@@ -93,8 +103,8 @@ moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* o
     g.how_out = rows & MOE_ROWS_SCATTER ? moe::kRowSlot : moe::kRowSorted;
     g.out = out;
     (void)hipGetLastError();
-    if (dx) moe::launch_grouped_dx(g, (hipStream_t)stream);
-    else moe::launch_grouped_fwd(g, (hipStream_t)stream);
+    if (dx) moe::launch_grouped_dx(g, workspace, (hipStream_t)stream);
+    else moe::launch_grouped_fwd(g, workspace, (hipStream_t)stream);
     return finish();
 }
 
@@ -102,17 +112,19 @@ moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* o
 
 MOE_API moe_status moe_grouped_gemm(const void* x, const void* w, const int32_t* expert_offsets,
                                     const int32_t* sorted_ids, int rows, int T, int topk, int R,
-                                    int E, int K, int N, void* y, void* stream) {
+                                    int E, int K, int N, void* y, void* workspace,
+                                    size_t* workspace_bytes, void* stream) {
     return grouped_rows(false, x, w, expert_offsets, sorted_ids, rows, T, topk, R, E, K, N, y,
-                        stream);
+                        workspace, workspace_bytes, stream);
 }
 
 MOE_API moe_status moe_grouped_gemm_dx(const void* dy, const void* w,
                                        const int32_t* expert_offsets, const int32_t* sorted_ids,
                                        int rows, int T, int topk, int R, int E, int K, int N,
-                                       void* dx, void* stream) {
+                                       void* dx, void* workspace, size_t* workspace_bytes,
+                                       void* stream) {
     return grouped_rows(true, dy, w, expert_offsets, sorted_ids, rows, T, topk, R, E, K, N, dx,
-                        stream);
+                        workspace, workspace_bytes, stream);
 }
 
 MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
@@ -132,7 +144,7 @@ MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
         return MOE_ERR_UNSUPPORTED;
     g.out_f32 = out != MOE_OUT_BF16;
     g.accumulate = out == MOE_OUT_FP32_ADD;
-    if (workspace_step(workspace, workspace_bytes, round_up(moe::grouped_dw_workspace(g)), &st))
+    if (workspace_step(workspace, workspace_bytes, product_size(moe::grouped_dw_workspace(g)), &st))
         return st;
     if (R == 0 && g.accumulate) return MOE_OK;
     if (!expert_offsets || !dw) return MOE_ERR_INVALID_ARG;

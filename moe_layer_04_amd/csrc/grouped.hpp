@@ -40,6 +40,17 @@ __device__ __forceinline__ int grouped_offset_scalar(const GroupedArgs& g, int e
     return min(max(((scalar_t)g.offsets)[e], 0), g.R);
 }
 
+// Rows products cut into g.splits ranges of the reduction leave an fp32 product
+// [R, grouped_part_ld(width)] a range; rows stay 16-byte aligned.
+__host__ __device__ inline int grouped_part_ld(int width) { return (width + 3) / 4 * 4; }
+// range sp's steps [first, first + count) of `steps`
+struct GroupedRange { int first, count; };
+__host__ __device__ inline GroupedRange grouped_range(int steps, int splits, int sp) {
+    const int per = (steps + splits - 1) / splits;
+    const int first = sp * per < steps ? sp * per : steps;
+    return {first, steps - first < per ? steps - first : per};
+}
+
 struct GroupedBlock {
     int e;       // expert, -1: no such block
     int row0;    // first sorted row of the block

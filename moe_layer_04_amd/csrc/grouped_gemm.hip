@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
     const int a_dim = OP == kOpFwd ? g.N : g.K;
     const int a_tiles = (a_dim + kSim - 1) / kSim;
     const int a0 = ((int)blockIdx.x % a_tiles) * kSim;  // first output column
-    const int bt = (int)blockIdx.x / a_tiles;
+    int bt = (int)blockIdx.x / a_tiles, sp = 0;
     int e, row0, rows, b0 = 0, red;
     if constexpr (OP == kOpDw) {
         const int n_tiles = (g.N + kSim - 1) / kSim;
@@ -120,6 +120,8 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
         red = rows;
         if (rows == 0 && g.accumulate) return;
     } else {
+        sp = bt % g.splits;
+        bt /= g.splits;
         const GroupedBlock b = grouped_find(grouped_scan(g, kSim), bt, kSim);
         if (b.e < 0) return;
         e = b.e;
@@ -194,18 +196,23 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
     for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < 2; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
-    const int steps = (red + kSim - 1) / kSim;
+    int first = 0, steps = (red + kSim - 1) / kSim;
+    if constexpr (OP != kOpDw) {
+        const GroupedRange range = grouped_range(steps, g.splits, sp);
+        first = range.first;
+        steps = range.count;
+    }
     Step ahead[kSimAhead];
 #pragma unroll
     for (int i = 0; i < kSimAhead; ++i)
-        if (i < steps) ahead[i] = load(i);
+        if (i < steps) ahead[i] = load(first + i);
     for (int s0 = 0; s0 < steps; s0 += kSimAhead) {
 #pragma unroll
         for (int i = 0; i < kSimAhead; ++i) {
             const int s = s0 + i;
             if (s >= steps) break;
             char* buf = lds[s & 1];
-            settle(ahead[i], s);
+            settle(ahead[i], first + s);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 *reinterpret_cast<u16x8_t*>(buf + sim_at<ACOL>(r + 32 * h, c)) = ahead[i].a[h];
@@ -213,7 +220,7 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
             }
             // the buffer written next was last read before this barrier
             __syncthreads();
-            if (s + kSimAhead < steps) ahead[i] = load(s + kSimAhead);
+            if (s + kSimAhead < steps) ahead[i] = load(first + s + kSimAhead);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 bf16x8_t fa[2], fb[2];
@@ -239,7 +246,7 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
             dst = ((size_t)e * g.N + b0 + j) * g.K;
         } else {
             int row = row0 + j;
-            if (g.how_out == kRowSlot) {
+            if (g.splits == 1 && g.how_out == kRowSlot) {
                 row = grouped_row(g, row, kRowSlot);
                 if (row < 0) continue;
             }
@@ -251,7 +258,11 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
             f32x4_t v = acc[a][b];
             typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
             typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
-            if (OP == kOpDw && g.out_f32) {
+            if (OP != kOpDw && g.splits > 1) {
+                if (col < a_dim)
+                    *reinterpret_cast<f32x4_t*>((float*)g.out + ((size_t)sp * g.R + row0 + j) *
+                                                grouped_part_ld(a_dim) + col) = v;
+            } else if (OP == kOpDw && g.out_f32) {
                 float* o = (float*)g.out + dst + col;
                 if (col + 4 <= a_dim) {
                     f32x4_any_t* p = reinterpret_cast<f32x4_any_t*>(o);
@@ -288,54 +299,147 @@ bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
 template <int OP>
 void launch_small(const GroupedArgs& g, hipStream_t s) {
     const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + kSim - 1) / kSim;
-    const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSim - 1) / kSim) : blocks_bound(g, kSim);
+    const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSim - 1) / kSim) : blocks_bound(g, kSim) * g.splits;
     if (chunked(g)) grouped_small_kernel<OP, true><<<a_tiles * b_tiles, 256, 0, s>>>(g);
     else grouped_small_kernel<OP, false><<<a_tiles * b_tiles, 256, 0, s>>>(g);
 }
 
 }  // namespace
 
-// Row products on full tiles, one a CU, unless the small tiles are few: up to
-// two a CU their shorter step wins (about 0.6-1 us against 1.3-1.5 us), beyond
-// it the larger tiles' reuse does.  us, small / full tiles, T tokens x k over E
-// experts (in brackets: small tiles):
-//   fwd N x K  1x2/16 16384x4096 [512] 44.9/54.4;  512x2/8 2048x1024 [512] 16.9/21.8;
-//              64x2/8 14336x4096 [1792] 204/160;  2048x2/8 2048x1024 [2048] 42.3/25.6
-//   dx  N x K  8x2/8 28672x4096 [512] 349/409;  128x2/8 14336x4096 [512] 199/214;
-//              256x2/8 14336x4096 [512] 253/237;  2048x2/8 1024x256 [256] 15.3/23.6;
-//              2048x2/8 2048x1024 [1024] 52.4/40.6;  8192x2/8 512x256 [1024] 19.4/17.0
-static bool full_tiles(const GroupedArgs& g, int cols) {
-    if (!chunked(g)) return false;
-    const long experts = g.R < g.E ? g.R : g.E, blocks = g.R / kSim;
-    return (long)((cols + kSim - 1) / kSim) * (blocks > experts ? blocks : experts) > 512;
+namespace {
+// y = the ranges' products added up in order, a thread per four values; row i
+// goes where the product would have put it
+__global__ __launch_bounds__(256) void rows_join_kernel(const float* __restrict__ parts, GroupedArgs g,
+                                                        int width) {
+    const int ld = grouped_part_ld(width);
+    const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+    const int i = (int)(at / (uint32_t)(ld / 4)), col = (int)(at % (uint32_t)(ld / 4)) * 4;
+    if (i >= g.R || i < grouped_offset(g, 0) || i >= grouped_offset(g, g.E)) return;
+    const int row = g.how_out == kRowSlot ? grouped_row(g, i, kRowSlot) : i;
+    if (row < 0) return;
+    const float* p = parts + (size_t)i * ld + col;
+    const size_t next = (size_t)g.R * ld;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll 4
+    for (int s = 1; s < g.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(p + s * next);
+    uint16_t* o = (uint16_t*)g.out + (size_t)row * width + col;
+    typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
+    u16x4_t q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = f32_to_bf16_bits(v[j]);
+    if (col + 4 <= width) {
+        *reinterpret_cast<u16x4_any_t*>(o) = q;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (col + j < width) o[j] = q[j];
+    }
 }
 
-// The weight stream while an expert has up to three rows on average; us, stream
-// / best of the tiles: 1x2/16 16384x4096 49/57, 8x2/8 28672x4096 286/317,
-// 16x8/64 1024x2048 44/59; at four rows 16x2/8 28672x4096 317/324 and 128x8/256
-// 7168x2048 1277/1257, at eight 32x2/8 28672x4096 339/324.
-static bool stream(const GroupedArgs& g) {
-    return chunked(g) && g.R <= 3L * (g.R < g.E ? g.R : g.E);
+// How a rows product is computed: on which tiles, and in how many ranges of its
+// reduction.  us; (tokens x k / experts, reduction -> columns).
+//
+// The weight stream (forward) while an expert has up to three rows on average.
+// Stream / best of the tiles: 1x2/16 4096->16384 40/42, 8x2/8 4096->28672
+// 286/317, 1x1/1 4096->4096 11.1/13.1; at four rows 16x2/8 4096->28672 317/324
+// and 128x8/256 2048->7168 1277/1257, at eight 32x2/8 4096->28672 339/324.  In
+// ranges up to a workgroup a CU, if a wave has 32 steps or more to share:
+// 1x6/21 10328->272 18.9 whole, 13.5 in four; 1x1/1 14336->4096 30.7, 22.1 in
+// two, but 1x1/1 4096->4096 11.1, 13.7 in two (the second launch).
+//
+// Full tiles above 512 small ones, or fewer with so many steps that ranges of
+// them fill the chip.  Small / full, each in its best number of ranges:
+//   fwd 512x2/8   1024->2048 16.3/21.9,   4096->2048 49.8/40.7,  14336->2048 188/114
+//       1024x1/1  1024->1024 9.9/22.4,    4096->1024 25.2/29.9,  14336->1024 62.9/46.3
+//                 1024->4096 19.8/23.3,   2048->4096 33.8/36.6,  4096->4096 63.1/49.2
+//   dx  2048x2/8  1024->512 17.7/24.4,    2048->512 29.5/29.0,   14336->512 186/89
+//                 1024->1024 28.5/25.4,   4096->1024 85.1/53.7
+//       37x8/8    14336->512 33.9/33.3,   14336->1024 49.2/44.0, 14336->2048 102/93
+//       8x2/8     28672->4096 313/269;    8192x2/8 512->256 19.2/16.5
+//
+// Ranges of full tiles while a CU has no more than one and a range 16 steps:
+// 1024x1/1 14336->1024 214 whole, 68.6 in four, 46.3 in eight; 4096->4096 67.1,
+// 51.4, 49.2 (two, four); two ranges of 8 steps 1024->4096 23.3, 29.6.  Of small
+// tiles while a CU has no more than two, a range eight steps and the whole 32:
+// 1024x1/1 4096->512 34.9 whole, 18.7 in four, 21.1 in eight; 2048->512 19.4,
+// 13.7, 16.1; 1024->512 9.8, 13.4 (four).
+struct RowsPlan {
+    enum { kStream, kFull, kSmall } on;
+    int splits;
+};
+RowsPlan rows_plan(const GroupedArgs& g, bool dx) {
+    const int cols = dx ? g.K : g.N;
+    const long steps = ((dx ? g.N : g.K) + 63) / 64;  // of either tiles and of the stream
+    const long experts = g.R < g.E ? g.R : g.E;
+    const long small_blocks = g.R / kSim, full_blocks = g.R / 256 + experts / 2;
+    const long small = (long)((cols + 63) / 64) * (small_blocks > experts ? small_blocks : experts);
+    const long full = (long)((cols + 255) / 256) * (full_blocks > experts ? full_blocks : experts);
+    RowsPlan p = {RowsPlan::kSmall, 1};
+    if (chunked(g) && !dx && g.R <= 3 * experts) p.on = RowsPlan::kStream;
+    else if (chunked(g) && (small > 512 || small * steps >= 512 * 64)) p.on = RowsPlan::kFull;
+    long work, most, least;  // workgroups whole, the most of them, a range's least steps
+    if (p.on == RowsPlan::kStream) {
+        work = (long)((cols + 31) / 32) * experts;
+        most = 256;
+        least = steps < 128 ? steps : 32;
+    } else if (p.on == RowsPlan::kFull) {
+        work = full;
+        most = 256;
+        least = 16;
+    } else {
+        work = small;
+        most = 512;
+        least = steps < 32 ? steps : 8;
+    }
+    while (p.splits < 16 && work * p.splits * 2 <= most && steps / (p.splits * 2) >= least) p.splits *= 2;
+    return p;
 }
 
-void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s) {
-    if (stream(g)) launch_grouped_stream_fwd(g, s);
-    else if (full_tiles(g, g.N)) launch_grouped_tiles_fwd(g, s);
-    else launch_small<kOpFwd>(g, s);
+size_t rows_workspace(const GroupedArgs& g, bool dx) {
+    if (g.R == 0) return 0;
+    const int splits = rows_plan(g, dx).splits;
+    return splits > 1 ? (size_t)splits * g.R * grouped_part_ld(dx ? g.K : g.N) * 4 : 0;
 }
-void launch_grouped_dx(const GroupedArgs& g, hipStream_t s) {
-    if (full_tiles(g, g.K)) launch_grouped_tiles_dx(g, s);
-    else launch_small<kOpDx>(g, s);
+
+template <bool DX>
+void launch_rows(const GroupedArgs& call, void* workspace, hipStream_t s) {
+    GroupedArgs g = call;
+    const RowsPlan plan = rows_plan(g, DX);
+    g.splits = plan.splits;
+    if (g.splits > 1) g.out = workspace;
+    if (plan.on == RowsPlan::kStream) launch_grouped_stream_fwd(g, s);
+    else if (plan.on == RowsPlan::kSmall) launch_small<DX ? kOpDx : kOpFwd>(g, s);
+    else if (DX) launch_grouped_tiles_dx(g, s);
+    else launch_grouped_tiles_fwd(g, s);
+    if (g.splits > 1) {
+        const int width = DX ? g.K : g.N;
+        const long threads = (long)g.R * (grouped_part_ld(width) / 4);
+        g.out = call.out;
+        rows_join_kernel<<<(int)((threads + 255) / 256), 256, 0, s>>>((const float*)workspace, g, width);
+    }
 }
-// The weight gradient on small tiles: up to four a CU, while the rows of an
-// expert are few (a full tile's start costs more than its steps there).  Kernel
-// us, small / full tiles, rows over E experts of N x K (small tiles): 666/8
-// 1032x256 [544] 9.4/15.6, 666/8 1032x512 [1088] 11.2/14.6, 2000/8 1024x256
-// [512] 17.4/24.2, 300/2 1024x1024 [512] 9.3/15.6, 1024/8 2048x1024 [4096] 34/16.
+}  // namespace
+
+size_t grouped_fwd_workspace(const GroupedArgs& g) { return rows_workspace(g, false); }
+size_t grouped_dx_workspace(const GroupedArgs& g) { return rows_workspace(g, true); }
+void launch_grouped_fwd(const GroupedArgs& g, void* workspace, hipStream_t s) {
+    launch_rows<false>(g, workspace, s);
+}
+void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
+    launch_rows<true>(g, workspace, s);
+}
+
+// The weight gradient on small tiles: up to ten a CU, while the rows of an
+// expert are few (a full tile's start costs more than its steps there).  us,
+// small / full tiles, rows over E experts of N x K (small tiles): 666/8 1032x256
+// [544] 9.4/15.6, 300/2 1024x1024 [512] 9.3/15.6, 64/8 1024x1024 [2048]
+// 10.2/11.3, 1024/8 the same 14.7/15.2, 19/38 2056x128 [2508] 10.2/31.7; 180/23
+// 640x768 [2760] 11.3/13.7, 1024/8 2048x1024 [4096] 34/16, 512/64 2048x512
+// [16384] 47/27; 16625/41 120x1728 [2214] 37.7/32.6.
 static bool small_dw(const GroupedArgs& g) {
     if (!chunked(g)) return true;
     const long tiles = (long)((g.K + kSim - 1) / kSim) * ((g.N + kSim - 1) / kSim) * g.E;
-    return tiles <= 1088 && g.R <= 256L * (g.R < g.E ? g.R : g.E);
+    return tiles <= 2560 && g.R <= 256L * (g.R < g.E ? g.R : g.E);
 }
 size_t grouped_dw_workspace(const GroupedArgs& g) {
     const int splits = small_dw(g) || g.R == 0 ? 1 : grouped_tiles_dw_splits(g);

@@ -4,8 +4,11 @@
 // cores, bound by HBM reads.
 //
 // A workgroup of four waves takes 32 rows of W[e] against one block of up to 16
-// rows of x, a quarter of the reduction a wave.  No LDS in the main loop: a
-// wave loads its fragments straight into registers, two steps ahead.
+// rows of x, a quarter of the reduction a wave; of a short reduction 32 rows a
+// wave (280 rows over 200 experts, us, quarters / whole: 15168 x 192 390/198,
+// 4096 x 512 143/112, 4096 x 1024 226/213, but 512 x 1024 29.7/31.7).  No LDS in
+// the main loop: a wave loads its fragments straight into registers, two steps
+// ahead.
 // 16x16x32 MFMA: lane l supplies row l % 16, reduction 8*(l/16)..+8, so a load
 // instruction takes 64 bytes of each of 16 rows; a step is 64 reduction
 // elements, 128 bytes a row.  x comes from L2 (a block's rows are read by every
@@ -32,15 +35,22 @@ namespace {
 
 constexpr uint32_t kNowhere = 0x80000000u;
 constexpr int kRowsA = 32, kRowsB = 16, kStep = 64, kWaves = 4, kAhead = 2;
+constexpr int kWhole = 512;  // longest reduction that a wave takes whole
 
+// QUARTERS: a wave takes a quarter of the reduction, else all of it for 32 rows
+// of its own
+template <bool QUARTERS>
 __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs g) {
-    __shared__ f32x4_t part[kWaves - 1][2][64];
+    __shared__ f32x4_t part[QUARTERS ? kWaves - 1 : 1][2][64];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    const int a_tiles = (g.N + kRowsA - 1) / kRowsA;
-    const GroupedBlock blk = grouped_find(grouped_scan(g, kRowsB), (int)blockIdx.x / a_tiles, kRowsB);
+    constexpr int kRowsGroup = QUARTERS ? kRowsA : kRowsA * kWaves;
+    const int a_tiles = (g.N + kRowsGroup - 1) / kRowsGroup;
+    const int bt = (int)blockIdx.x / a_tiles, sp = bt % g.splits;
+    const GroupedBlock blk = grouped_find(grouped_scan(g, kRowsB), bt / g.splits, kRowsB);
     if (blk.e < 0) return;
-    const int a0 = ((int)blockIdx.x % a_tiles) * kRowsA;
+    const int a0 = ((int)blockIdx.x % a_tiles) * kRowsGroup + (QUARTERS ? 0 : wave * kRowsA);
+    if (!QUARTERS && a0 >= g.N) return;
     const uint32_t ld = (uint32_t)g.K * 2;
     const prsrc_t rw = pmake_rsrc(g.w + ((size_t)blk.e * g.N + a0) * g.K,
                                   (uint32_t)min(g.N - a0, kRowsA) * ld);
@@ -71,12 +81,13 @@ __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs
         return f;
     };
     f32x4_t acc[2] = {};
-    const int steps = (g.K + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
+    const int parts = QUARTERS ? kWaves * g.splits : 1, first = QUARTERS ? sp * kWaves + wave : 0;
+    const int steps = (g.K + kStep - 1) / kStep, per = (steps + parts - 1) / parts;
     const int turn = ((int)blockIdx.x * 7 + wave * 3) % per;
     // the wave's s-th step; past its quarter: a step past the reduction
     auto step = [&](int s) {
         const int t = s + turn;
-        return s < per ? wave * per + (t < per ? t : t - per) : kWaves * per;
+        return s < per ? first * per + (t < per ? t : t - per) : parts * per;
     };
     Frags ahead[kAhead];
 #pragma unroll
@@ -95,25 +106,33 @@ __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs
                         __builtin_bit_cast(bf16x8_t, f.x[h]), acc[a], 0, 0, 0);
         }
     }
-    if (wave > 0) {
+    if constexpr (QUARTERS) {
+        if (wave > 0) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) part[wave - 1][a][lane] = acc[a];
+            for (int a = 0; a < 2; ++a) part[wave - 1][a][lane] = acc[a];
+        }
+        __syncthreads();
+        if (wave > 0) return;
     }
-    __syncthreads();
-    if (wave > 0 || li >= blk.rows) return;
+    if (li >= blk.rows) return;
     // rows 16a + 4*(lane/16) + v of W, row lane % 16 of the block
     int row = blk.row0 + li;
-    if (g.how_out == kRowSlot) {
+    if (g.splits == 1 && g.how_out == kRowSlot) {
         row = grouped_row(g, row, kRowSlot);
         if (row < 0) return;
     }
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
         f32x4_t v = acc[a];
+        if constexpr (QUARTERS) {
 #pragma unroll
-        for (int w = 0; w < kWaves - 1; ++w) v += part[w][a][lane];
+            for (int w = 0; w < kWaves - 1; ++w) v += part[w][a][lane];
+        }
         const int n = a0 + 16 * a + 4 * q;
-        if (n < g.N)  // N is a multiple of 8
+        if (n >= g.N) continue;  // N is a multiple of 8
+        if (g.splits > 1)
+            *reinterpret_cast<f32x4_t*>((float*)g.out + ((size_t)sp * g.R + row) * g.N + n) = v;
+        else
             *reinterpret_cast<uint2*>((uint16_t*)g.out + (size_t)row * g.N + n) =
                 uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
@@ -122,9 +141,14 @@ __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs
 }  // namespace
 
 void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s) {
-    const int a_tiles = (g.N + kRowsA - 1) / kRowsA;
     const int blocks = g.R / kRowsB + (g.R < g.E ? g.R : g.E);
-    grouped_stream_kernel<<<a_tiles * blocks, kWaves * 64, 0, s>>>(g);
+    if (g.splits > 1 || g.K > kWhole) {
+        const int a_tiles = (g.N + kRowsA - 1) / kRowsA;
+        grouped_stream_kernel<true><<<a_tiles * blocks * g.splits, kWaves * 64, 0, s>>>(g);
+    } else {
+        const int a_tiles = (g.N + kRowsA * kWaves - 1) / (kRowsA * kWaves);
+        grouped_stream_kernel<false><<<a_tiles * blocks, kWaves * 64, 0, s>>>(g);
+    }
 }
 
 }  // namespace moe

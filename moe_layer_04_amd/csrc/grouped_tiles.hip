@@ -53,6 +53,7 @@ typedef uint32_t Offsets[kInstr];
 struct RowCopy {
     prsrc_t r;
     uint32_t red_bytes;
+    int first = 0;        // step of the reduction that counts as step 0
 
     // row of the tile that the lane's copy q fills, and its chunk of the
     // row: physical chunk lane % 8; the swizzle is the same for every q
@@ -64,7 +65,7 @@ struct RowCopy {
     }
     __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
         typedef __attribute__((address_space(3))) void* lds_ptr_t;
-        const uint32_t kb = (uint32_t)step * (kStep * 2);
+        const uint32_t kb = (uint32_t)(first + step) * (kStep * 2);
         // the last step of a reduction that is no multiple of 64
         const bool cut = kb + kStep * 2 > red_bytes && kb + chunk(gw, late_lane()) >= red_bytes;
 #pragma unroll
@@ -82,6 +83,7 @@ struct ColCopy {
     uint32_t ld;          // bytes a row
     uint32_t col0;        // bytes before the tile's first column in a row
     int red;              // rows
+    int first = 0;        // step of the reduction that counts as step 0
 
     // the lane's chunk of its row at copy q
     __device__ static __forceinline__ uint32_t chunk(int q, int lane) {
@@ -105,7 +107,7 @@ struct ColCopy {
     // the descriptor starts at the step's first row, so that offsets stay
     // small however many rows there are
     __device__ __forceinline__ void copy(const Offsets& off, char* slot, int step, int gw) const {
-        const int row0 = step * kStep;
+        const int row0 = (first + step) * kStep;
         const uint32_t rows = (uint32_t)min(red - row0, kStep);
         issue(pmake_rsrc(base + (size_t)row0 * ld, rows * ld - col0), off, slot, gw);
     }
@@ -271,14 +273,15 @@ struct PingPong {
 constexpr int kStRow = 256 + 16, kStArea = 64 * kStRow + 64 * 8;
 static_assert(4 * kStArea <= kLds, "the staging fits the slots");
 
+template <bool F32>
 __device__ __forceinline__ void store_tile(char* st, const f32x16_t (&acc)[4][2], long dst, int c0,
-                                           int cols, void* out, int out_f32, int accumulate) {
+                                           int cols, void* out) {
     const int lane = late_lane();
     const int li = lane & 31, half = lane >> 5, rr = lane >> 4, c = lane & 15;
     long* place = reinterpret_cast<long*>(st + 64 * kStRow);
     lds_wave_fence();
     place[lane] = dst;
-    if (out_f32) {
+    if constexpr (F32) {
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
@@ -297,13 +300,9 @@ __device__ __forceinline__ void store_tile(char* st, const f32x16_t (&acc)[4][2]
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
                 const int row = 4 * i + rr;
-                f32x4_t v = *reinterpret_cast<const f32x4_t*>(st + row * kStRow + c * 16);
+                const f32x4_t v = *reinterpret_cast<const f32x4_t*>(st + row * kStRow + c * 16);
                 const long d = place[row];
-                if (d >= 0 && col < cols) {
-                    f32x4_t* p = reinterpret_cast<f32x4_t*>((float*)out + d + col);
-                    if (accumulate) v = *p + v;
-                    *p = v;
-                }
+                if (d >= 0 && col < cols) *reinterpret_cast<f32x4_t*>((float*)out + d + col) = v;
             }
             lds_wave_fence();
         }
@@ -340,7 +339,10 @@ __device__ __forceinline__ void store_tile(char* st, const f32x16_t (&acc)[4][2]
 // the experts' row blocks, so that the workgroups resident on an XCD share the
 // weights and rows they copy in its L2.  The number of row blocks is known on
 // the device only: the grid covers the most there can be.
-template <bool DX, bool LOOK>
+//
+// Few tiles: PARTS cuts the reduction into g.splits ranges, each of which
+// stores its fp32 product of the tile; rows_join adds them up.
+template <bool DX, bool LOOK, bool PARTS>
 __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const int lane = lane_id();
@@ -349,11 +351,13 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     const int cols = DX ? g.K : g.N, red = DX ? g.N : g.K;
     const int a_tiles = (cols + kTile - 1) / kTile;
     const GroupedScan scan = grouped_scan(g, kTile);
-    const int total = a_tiles * scan.total;
+    const int tiles = a_tiles * scan.total, total = PARTS ? tiles * g.splits : tiles;
     const int per_xcd = (total + 7) / 8;
     const int local = (int)blockIdx.x / 8;
-    const int t = ((int)blockIdx.x % 8) * per_xcd + local;
+    int t = ((int)blockIdx.x % 8) * per_xcd + local;
     if (local >= per_xcd || t >= total) return;
+    const int sp = PARTS ? t / tiles : 0;
+    if constexpr (PARTS) t %= tiles;
     const int span = kGroup * scan.total;
     const int grp = t / span, in = t % span;
     const int gsize = min(kGroup, a_tiles - grp * kGroup);
@@ -405,7 +409,12 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     // wave tile: 128 columns x 64 rows, 2 x 2 waves in each half of the rows
     const int arow0 = (gw & 1) * 128, brow0 = (wave >> 2) * 128 + (gw >> 1) * 64;
     const bool used = brow0 < blk.rows;
-    const int steps = (red + kStep - 1) / kStep;
+    int steps = (red + kStep - 1) / kStep;
+    if constexpr (PARTS) {
+        const GroupedRange range = grouped_range(steps, g.splits, sp);
+        ca.first = cb.first = range.first;
+        steps = range.count;
+    }
     PingPong<DX, false, CopyA, RowCopy> core;
     if (used) core.template run<true>(lds, ca, cb, off, steps, wave, arow0, brow0);
     else core.template run<false>(lds, ca, cb, off, steps, wave, arow0, brow0);
@@ -413,9 +422,10 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
         const int j = brow0 + late_lane();
         long row = -1;
         if (j < blk.rows)
-            row = g.how_out == kRowSlot ? grouped_row(g, blk.row0 + j, kRowSlot) : blk.row0 + j;
-        store_tile(lds + gw * kStArea, core.acc, row < 0 ? -1 : row * cols, a0 + arow0, cols, g.out,
-                   0, 0);
+            row = !PARTS && g.how_out == kRowSlot ? grouped_row(g, blk.row0 + j, kRowSlot) : blk.row0 + j;
+        if (PARTS && row >= 0) row += (long)sp * g.R;
+        store_tile<PARTS>(lds + gw * kStArea, core.acc, row < 0 ? -1 : row * cols, a0 + arow0, cols,
+                          g.out);
     }
     core.finish(wave);
 }
@@ -823,9 +833,14 @@ template <bool DX>
 static void launch_rows_tiles(const GroupedArgs& g, hipStream_t s) {
     const int a_tiles = ((DX ? g.K : g.N) + kTile - 1) / kTile;
     const long most = (long)a_tiles * (g.R / kTile + (g.R < g.E ? g.R : g.E));
-    const int grid = (int)((most + 7) / 8 * 8);
-    if (rows_look(g, DX ? g.how_dy : g.how_x)) grouped_rows_kernel<DX, true><<<grid, 512, 0, s>>>(g);
-    else grouped_rows_kernel<DX, false><<<grid, 512, 0, s>>>(g);
+    const int grid = (int)((most * g.splits + 7) / 8 * 8);
+    auto run = [&](auto look, auto parts) {
+        grouped_rows_kernel<DX, decltype(look)::value, decltype(parts)::value><<<grid, 512, 0, s>>>(g);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (rows_look(g, DX ? g.how_dy : g.how_x)) g.splits > 1 ? run(yes, yes) : run(yes, no);
+    else g.splits > 1 ? run(no, yes) : run(no, no);
 }
 void launch_grouped_tiles_fwd(const GroupedArgs& g, hipStream_t s) { launch_rows_tiles<false>(g, s); }
 void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s) { launch_rows_tiles<true>(g, s); }

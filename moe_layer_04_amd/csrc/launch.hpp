@@ -175,11 +175,13 @@ struct GroupedArgs {
     uint32_t slots, magic;       // slots = T*topk; magic of grouped_token
     int T, R, E, K, N;
     int out_f32, accumulate;
-    int splits;                  // dw on full tiles: ranges of an expert's rows
-    void* out;
+    int splits;                  // ranges the reduction is cut into (dw: an expert's rows)
+    void* out;                   // splits > 1: the ranges' fp32 products
 };
-void launch_grouped_fwd(const GroupedArgs& g, hipStream_t s);
-void launch_grouped_dx(const GroupedArgs& g, hipStream_t s);
+void launch_grouped_fwd(const GroupedArgs& g, void* workspace, hipStream_t s);
+void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s);
+size_t grouped_fwd_workspace(const GroupedArgs& g);
+size_t grouped_dx_workspace(const GroupedArgs& g);
 // very few rows an expert (K and N multiples of 8)
 void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s);
 // full 256 x 256 tiles (K and N multiples of 8)

@@ -54,6 +54,16 @@ SHAPES = [
     (9, 2, 16, 2048, 8200, 1, (3,)),
     (20, 2, 16, 200, 40, 4, ()),             # the weight stream, padded, a reduction tail
     (23, 1, 23, 4096, 24, 1, (0, 22)),
+    (64, 1, 1, 2100, 13, 1, ()),             # few outputs of a long reduction: in ranges
+    (64, 1, 1, 13, 2100, 1, ()),
+    (70, 2, 2, 4096, 136, 16, ()),
+    (70, 2, 2, 136, 4104, 16, ()),
+    (2, 2, 8, 8200, 40, 4, ()),              # the same of the weight stream
+    (3, 1, 3, 8704, 1000, 1, (1,)),
+    (2100, 1, 2, 2056, 1032, 1, ()),         # and of full tiles
+    (1100, 2, 4, 1032, 2056, 64, (1,)),
+    (1030, 1, 1, 7304, 1096, 1, ()),
+    (1030, 1, 1, 1096, 7304, 1, ()),
 ]
 
 
@@ -213,6 +223,39 @@ def test_same_bits_every_time(moe):
     for _ in range(4):
         for a, b in zip(first, once()):
             assert torch.equal(a, b)
+
+
+def test_ranges_in_a_graph(moe):
+    """Products in ranges, captured: two graphs that replay in turn, with eager
+    calls between them."""
+    note("ranges in a graph")
+    T, K, N = 150, 4096, 200
+    off = torch.tensor([0, 70, 150], dtype=torch.int32, device="cuda")
+    w = bf16((2, N, K), 2, K ** -0.5)
+    xs = [bf16((T, K), 7), bf16((T, K), 8)]
+
+    def run(x):
+        return moe.moe_grouped_gemm(x, w, off)
+    want = [run(x).clone() for x in xs]
+    assert moe.moe_grouped_gemm(xs[0], w, off, workspace=torch.empty(
+        1 << 24, dtype=torch.uint8, device="cuda")).equal(want[0])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(xs[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(run(x))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, out, y in zip(graphs, outs, want):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(run(xs[1]), want[1])
+            torch.cuda.synchronize()
+            assert torch.equal(out, y)
 
 
 def test_two_streams(moe):

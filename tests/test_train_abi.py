@@ -21,22 +21,40 @@ def lib():
 
 @pytest.mark.parametrize("name", ["moe_grouped_gemm", "moe_grouped_gemm_dx"])
 def test_grouped_rows_refusals(lib, name):
+    n = ctypes.c_size_t(0)
+
     def call(a=FAKE, w=FAKE, off=FAKE, ids=FAKE, rows=1, T=8, topk=2, R=16, E=4, K=64, N=96,
-             out=FAKE):
-        return getattr(lib, name)(a, w, off, ids, rows, T, topk, R, E, K, N, out, None)
+             out=FAKE, ws=FAKE, nbytes=1 << 40):
+        n.value = nbytes
+        return getattr(lib, name)(a, w, off, ids, rows, T, topk, R, E, K, N, out, ws,
+                                  ctypes.byref(n), None)
 
     for kw in (dict(T=-1), dict(topk=0), dict(R=-1), dict(E=0), dict(K=0), dict(N=0),
                dict(rows=4), dict(rows=8), dict(ids=None), dict(ids=None, rows=2), dict(a=None),
                dict(w=None), dict(off=None), dict(out=None), dict(a=MISALIGNED),
                dict(w=MISALIGNED), dict(off=MISALIGNED), dict(ids=MISALIGNED),
-               dict(out=MISALIGNED)):
+               dict(out=MISALIGNED), dict(ws=ctypes.c_void_p(0x10010))):
         assert call(**kw) == INV, kw
+    assert getattr(lib, name)(FAKE, FAKE, FAKE, FAKE, 1, 8, 2, 16, 4, 64, 96, FAKE, FAKE, None,
+                              None) == INV
     for kw in (dict(E=257), dict(topk=17), dict(R=1 << 28), dict(T=1 << 27), dict(K=1 << 20),
                dict(N=1 << 20), dict(K=1 << 15, N=1 << 15),      # one expert's weights: 2 GiB
                dict(T=1 << 24, K=64, N=64),                       # the gathered rows: 2 GiB
                dict(R=(1 << 28) - 1, K=1 << 19, N=64, T=8, rows=0)):   # the grid
         assert call(**kw) == UNS, kw
     assert call(R=0, a=None, w=None, off=None, ids=None, out=None, rows=0) == OK
+    query = dict(a=None, w=None, off=None, ids=None, out=None, ws=None)
+    for rows in (0, 1, 2, 3):
+        assert call(**query, rows=rows) == OK
+        assert n.value == 256                                     # unused, never NULL-sized
+        assert call(rows=rows, nbytes=255) == WSP
+    # few output tiles of a long reduction: fp32 products of its ranges
+    red, cols = ("K", "N") if name == "moe_grouped_gemm" else ("N", "K")
+    for length, width, parts in ((2048, 8, 4), (2048, 7, 4), (4096, 2000, 8)):
+        assert call(**query, R=64, E=1, rows=0, **{red: length, cols: width}) == OK
+        assert n.value == parts * 64 * ((width + 3) // 4 * 4) * 4
+    assert call(**query, R=1, E=1, rows=0, **{red: 2048, cols: 1}) == OK
+    assert n.value == 512                                         # used, so not the least size
 
 
 def test_grouped_dw_refusals(lib):
