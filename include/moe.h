@@ -493,8 +493,8 @@ moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *exp
  *   dtopk_weights  out fp32 [slots], or NULL; slots that no row names stay as
  *                  they are
  *
- * Padding rows are written as zeros.  Errors: INVALID_ARG for null or
- * misaligned pointers, negative sizes, fewer slots than rows without
+ * Padding rows are written as zeros.  a and dg must not overlap an input.
+ * Errors: INVALID_ARG for null or misaligned pointers, negative sizes, fewer slots than rows without
  * sorted_ids, dtopk_weights without topk_weights; UNSUPPORTED for R or slots
  * >= 2^28 or N >= 2^20.
  */

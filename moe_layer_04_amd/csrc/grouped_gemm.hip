@@ -38,6 +38,11 @@ constexpr int kOpFwd = 0, kOpDx = 1, kOpDw = 2;
 //
 // 16x16x32: lane l supplies row l % 16, reduction 8*(l/16)..+8; its
 // accumulators are rows 4*(l/16)+v of column l % 16.
+//
+// Bound by the latency of a step, 0.5-0.6 us with up to two workgroups a CU
+// (1024 rows of one expert, 4096 -> 1024: 34.9 us for 64 steps).  406 rows over 7
+// experts of 1001 x 330, dx: 14.2 us for 16 steps; 666 rows over 8 experts, dw
+// of 1032 x 256 in fp32: 7.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kSim = 64;                       // tile and step
 constexpr int kSimBytes = kSim * kSim * 2;     // one operand's step
