@@ -454,10 +454,12 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
 // Looked-up rows: a step's slots come by scalar loads a phase before they are
 // used, their offsets are computed between the MFMAs of the compute phase.
 //
-// 8192 rows over 8 experts of 28672 x 4096: 1950-1980 us (980 TFLOP/s with 1.9 GB
-// of results; a library product of 8192^3 in this orientation 1037).  Bound by
-// LDS reads: both operands come through the transposing read, 8 bytes a lane,
-// and the matrix cores are 48 % busy; storing a tile adds 3-4 us to its 31.
+// 8192 rows over 8 experts of 28672 x 4096: 1780-1810 us (1070 TFLOP/s with 1.9
+// GB of results; a library product of 8192^3 in this orientation 1037).  What
+// costs is the ends of tiles of 16 steps: storing one adds 3-4 us to its 31
+// (32768 rows, 14336 x 4096: 3.05 ms, 1260 TFLOP/s).  Looked-up rows take 7 %
+// more (1930-1960 us): their scalar work is issued between the MFMAs, and with
+// half as much of it again they took 10 %.
 //
 // Tile order: each XCD takes an eighth of every expert's tiles (experts have
 // different numbers of rows; an expert to an XCD would leave most of them
@@ -691,10 +693,11 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
             }
         }
     };
-    // a row's place: the slot's token (a quotient, see grouped_token) or its
-    // position in the step, one of them masked out
-    const uint32_t quot = token ? g.magic : 0, self = token && !g.magic ? ~0u : 0,
-                   pos = token ? 0 : ~0u;
+    // a row's place: the slot's token (a quotient, see grouped_token; topk == 1
+    // as 2p * 2^31) or its position in the step.  Scalar work as far as it
+    // goes, and little of it: it has to fit between the MFMAs
+    const uint32_t quot = !token ? 0 : g.magic ? g.magic : 1u << 31, shift = token && !g.magic;
+    const uint32_t in_step = token ? 0 : (uint32_t)(gw * 16 + (lane >> 5)) * ld, two_rows = token ? 0 : 2 * ld;
     const uint32_t chunk0 = ColCopy::chunk(0, lane);
     // offsets of copy q from its two rows' slots
     auto place = [&](int q) {
@@ -703,12 +706,13 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t p = (uint32_t)ids[2 * q + h];
-                const uint32_t at = (__umulhi(p, quot) + (p & self) + ((gw * 16 + 2 * q + h) & pos)) * ld;
+                const uint32_t at = __umulhi(p << shift, quot) * ld;
                 o[h] = p < g.slots ? at : kNowhere;
             }
-            // (the chunk from its first form each time: held for every q it would
-            // cost registers that the loop does not have)
-            off[q] = (lane >> 5 ? o[1] : o[0]) + (fresh(chunk0) ^ (uint32_t)((q & 3) << 7));
+            // (from their first forms each time: held for every q they would cost
+            // registers that the loop does not have)
+            off[q] = (lane >> 5 ? o[1] : o[0]) + (fresh(in_step) + (uint32_t)q * two_rows) +
+                     (fresh(chunk0) ^ (uint32_t)((q & 3) << 7));
         }
     };
     auto place_all = [&]() {
@@ -786,8 +790,10 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
                         for (int b = 0; b < 2; ++b)
                             acc[a][b] = mfma32_bf16(fa[ks][a], fb[ks][b], acc[a][b]);
                         if constexpr (LOOK) {
-                            if (a & 1) place(ks * 2 + a / 2);
-                            __builtin_amdgcn_sched_barrier(0);
+                            if (a & 1) {
+                                place(ks * 2 + a / 2);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
                         }
                     }
             } else {
