@@ -24,12 +24,13 @@ constexpr int kOpFwd = 0, kOpDx = 1, kOpDw = 2;
 // each, 16x16x32 MFMAs), 64 reduction elements a step.  For products with too
 // few outputs for 256 x 256 tiles, where the time is the latency of a step, and
 // for rows that are not whole 16-byte chunks, which the copies of those tiles
-// cannot take.  A step's chunks of 8 elements are loaded into registers two
+// cannot take; for many outputs of such rows also as 128 x 128 (see wide).  A step's chunks of 8 elements are loaded into registers two
 // steps ahead (16 bytes at any 2-byte address; a row's last chunk element by
 // element, so that nothing past a row is read) and stored to one of two LDS
 // buffers, a barrier a step.
 //
-// LDS layouts, both 64 rows of 128 bytes.  Rows along the output (operands that
+// LDS layouts of 64 rows (or of 64 columns; 128 are two such parts), both 64
+// rows of 128 bytes.  Rows along the output (operands that
 // are contiguous in the reduction): 16-byte chunks permuted by the row as in
 // the full tiles, fragments read directly.  Rows along the reduction: fragments
 // come through the transposing read (lane i of 16 gets column i of four rows,
@@ -105,21 +106,25 @@ __device__ __forceinline__ bf16x8_t sim_frag(const char* buf, int first, int ks,
     }
 }
 
-template <int OP, bool WHOLE>
-__global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel(GroupedArgs g) {
+template <int OP, bool WHOLE, int TILE>
+__global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void grouped_small_kernel(
+    GroupedArgs g) {
     constexpr bool ACOL = OP != kOpFwd, BCOL = OP == kOpDw;
-    __shared__ __attribute__((aligned(16))) char lds[2][2 * kSimBytes];
+    constexpr int AHEAD = TILE > kSim && OP == kOpDw ? 1 : kSimAhead;
+    constexpr int SUBS = TILE / kSim, H = 2 * SUBS, F = TILE / 32;  // parts, chunks and fragments of an operand
+    constexpr int kOperand = SUBS * kSimBytes;
+    __shared__ __attribute__((aligned(16))) char lds[2][2 * kOperand];
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int a_dim = OP == kOpFwd ? g.N : g.K;
-    const int a_tiles = (a_dim + kSim - 1) / kSim;
-    const int a0 = ((int)blockIdx.x % a_tiles) * kSim;  // first output column
+    const int a_tiles = (a_dim + TILE - 1) / TILE;
+    const int a0 = ((int)blockIdx.x % a_tiles) * TILE;  // first output column
     int bt = (int)blockIdx.x / a_tiles, sp = 0;
     int e, row0, rows, b0 = 0, red;
     if constexpr (OP == kOpDw) {
-        const int n_tiles = (g.N + kSim - 1) / kSim;
+        const int n_tiles = (g.N + TILE - 1) / TILE;
         e = bt / n_tiles;
-        b0 = (bt % n_tiles) * kSim;
+        b0 = (bt % n_tiles) * TILE;
         row0 = grouped_offset_scalar(g, e);
         rows = max(grouped_offset_scalar(g, e + 1) - row0, 0);
         red = rows;
@@ -127,7 +132,7 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
     } else {
         sp = bt % g.splits;
         bt /= g.splits;
-        const GroupedBlock b = grouped_find(grouped_scan(g, kSim), bt, kSim);
+        const GroupedBlock b = grouped_find(grouped_scan(g, TILE), bt, TILE);
         if (b.e < 0) return;
         e = b.e;
         row0 = b.row0;
@@ -135,44 +140,59 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
         red = OP == kOpFwd ? g.K : g.N;
     }
     const uint16_t* w = g.w + (size_t)e * g.N * g.K;
-    const int b_rows = OP == kOpDw ? min(g.N - b0, kSim) : rows;
+    const int b_rows = OP == kOpDw ? min(g.N - b0, TILE) : rows;
 
-    // this thread's chunk c of rows r and r + 32 of either operand
+    // this thread's chunks of an operand: c of rows r + 32h, or, where the rows
+    // run along the reduction, c of the h/2-th 64 columns of rows r and r + 32
     const int r = tid >> 3, c = tid & 7;
-    const uint16_t* brow[2] = {nullptr, nullptr};  // fwd, dx: fixed rows of B
+    auto col_row = [&](int h) { return r + 32 * (h & 1); };
+    auto col_at = [&](int h) { return (h >> 1) * kSim + c * 8; };
+    const uint16_t* brow[H];  // fwd, dx: fixed rows of B
     if constexpr (OP != kOpDw) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
+            brow[h] = nullptr;
             const int j = r + 32 * h;
             const int row = j < rows ? grouped_row(g, row0 + j, OP == kOpFwd ? g.how_x : g.how_dy) : -1;
             if (row >= 0) brow[h] = (OP == kOpFwd ? g.x : g.dy) + (size_t)row * red;
         }
     }
-    struct Step { u16x8_t a[2], b[2]; };
+    struct Step { u16x8_t a[H], b[H]; };
     auto load = [&](int step) {
         Step s;
         const int r0 = step * kSim;
+        if constexpr (OP == kOpDw) {
+            int rx[2], ry[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = r + 32 * h;
-            if constexpr (OP == kOpDw) {
-                int rx = -1, ry = -1;
-                if (r0 + i < red) {
-                    rx = ry = row0 + r0 + i;
+            for (int i = 0; i < 2; ++i) {
+                const int at = r0 + col_row(i);
+                rx[i] = ry[i] = -1;
+                if (at < red) {
+                    rx[i] = ry[i] = row0 + at;
                     if (g.sorted) {  // one slot for both operands' rows
-                        const uint32_t p = (uint32_t)g.sorted[rx];
+                        const uint32_t p = (uint32_t)g.sorted[row0 + at];
                         const int t = (int)grouped_token(p, g.magic);
-                        rx = p >= g.slots ? -1 : g.how_x == kRowToken ? t : rx;
-                        ry = p >= g.slots ? -1 : g.how_dy == kRowToken ? t : ry;
+                        rx[i] = p >= g.slots ? -1 : g.how_x == kRowToken ? t : rx[i];
+                        ry[i] = p >= g.slots ? -1 : g.how_dy == kRowToken ? t : ry[i];
                     }
                 }
-                s.a[h] = load_chunk<WHOLE>(rx < 0 ? nullptr : g.x + (size_t)rx * g.K, a0 + c * 8, g.K);
-                s.b[h] = load_chunk<WHOLE>(ry < 0 ? nullptr : g.dy + (size_t)ry * g.N, b0 + c * 8, g.N);
-            } else {
-                if constexpr (OP == kOpFwd)
-                    s.a[h] = load_chunk<WHOLE>(a0 + i < g.N ? w + (size_t)(a0 + i) * g.K : nullptr, r0 + c * 8, red);
-                else
-                    s.a[h] = load_chunk<WHOLE>(r0 + i < red ? w + (size_t)(r0 + i) * g.K : nullptr, a0 + c * 8, g.K);
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int x = rx[h & 1], y = ry[h & 1];
+                s.a[h] = load_chunk<WHOLE>(x < 0 ? nullptr : g.x + (size_t)x * g.K, a0 + col_at(h), g.K);
+                s.b[h] = load_chunk<WHOLE>(y < 0 ? nullptr : g.dy + (size_t)y * g.N, b0 + col_at(h), g.N);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if constexpr (OP == kOpFwd) {
+                    const int n = a0 + r + 32 * h;
+                    s.a[h] = load_chunk<WHOLE>(n < g.N ? w + (size_t)n * g.K : nullptr, r0 + c * 8, red);
+                } else {
+                    const int n = r0 + col_row(h);
+                    s.a[h] = load_chunk<WHOLE>(n < red ? w + (size_t)n * g.K : nullptr, a0 + col_at(h), g.K);
+                }
                 s.b[h] = load_chunk<WHOLE>(brow[h], r0 + c * 8, red);
             }
         }
@@ -180,70 +200,74 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
     };
     // whether a step has chunks to settle: last columns of the tile, or the end
     // of a reduction that runs along the rows
-    const bool a_ends = ACOL && a0 + kSim > g.K, b_ends = BCOL && b0 + kSim > g.N;
+    const bool a_ends = ACOL && a0 + TILE > g.K, b_ends = BCOL && b0 + TILE > g.N;
     auto settle = [&](Step& s, int step) {
         if constexpr (WHOLE) return;
         const int r0 = step * kSim;
         if (a_ends || (!ACOL && r0 + kSim > red)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s.a[h] = settle_chunk(s.a[h], (ACOL ? a0 : r0) + c * 8, ACOL ? g.K : red);
+            for (int h = 0; h < H; ++h)
+                s.a[h] = settle_chunk(s.a[h], ACOL ? a0 + col_at(h) : r0 + c * 8, ACOL ? g.K : red);
         }
         if (b_ends || (!BCOL && r0 + kSim > red)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s.b[h] = settle_chunk(s.b[h], (BCOL ? b0 : r0) + c * 8, BCOL ? g.N : red);
+            for (int h = 0; h < H; ++h)
+                s.b[h] = settle_chunk(s.b[h], BCOL ? b0 + col_at(h) : r0 + c * 8, BCOL ? g.N : red);
         }
     };
-    const int fa0 = (wave & 1) * 32, fb0 = (wave >> 1) * 32;
-    f32x4_t acc[2][2];
+    const int fa0 = (wave & 1) * (TILE / 2), fb0 = (wave >> 1) * (TILE / 2);
+    f32x4_t acc[F][F];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < F; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
+        for (int b = 0; b < F; ++b) acc[a][b] = f32x4_t{0, 0, 0, 0};
     int first = 0, steps = (red + kSim - 1) / kSim;
     if constexpr (OP != kOpDw) {
         const GroupedRange range = grouped_range(steps, g.splits, sp);
         first = range.first;
         steps = range.count;
     }
-    Step ahead[kSimAhead];
+    Step ahead[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kSimAhead; ++i)
+    for (int i = 0; i < AHEAD; ++i)
         if (i < steps) ahead[i] = load(first + i);
-    for (int s0 = 0; s0 < steps; s0 += kSimAhead) {
+    for (int s0 = 0; s0 < steps; s0 += AHEAD) {
 #pragma unroll
-        for (int i = 0; i < kSimAhead; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             const int s = s0 + i;
             if (s >= steps) break;
             char* buf = lds[s & 1];
             settle(ahead[i], first + s);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                *reinterpret_cast<u16x8_t*>(buf + sim_at<ACOL>(r + 32 * h, c)) = ahead[i].a[h];
-                *reinterpret_cast<u16x8_t*>(buf + kSimBytes + sim_at<BCOL>(r + 32 * h, c)) = ahead[i].b[h];
+            for (int h = 0; h < H; ++h) {
+                // the h/2-th 64 rows or columns
+                char* to = buf + (h >> 1) * kSimBytes;
+                *reinterpret_cast<u16x8_t*>(to + sim_at<ACOL>(col_row(h), c)) = ahead[i].a[h];
+                *reinterpret_cast<u16x8_t*>(to + kOperand + sim_at<BCOL>(col_row(h), c)) = ahead[i].b[h];
             }
             // the buffer written next was last read before this barrier
             __syncthreads();
-            if (s + kSimAhead < steps) ahead[i] = load(first + s + kSimAhead);
+            if (s + AHEAD < steps) ahead[i] = load(first + s + AHEAD);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bf16x8_t fa[2], fb[2];
+                bf16x8_t fa[F], fb[F];
+                const char* pa = buf + fa0 / kSim * kSimBytes;
+                const char* pb = buf + kOperand + fb0 / kSim * kSimBytes;
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    fa[f] = sim_frag<ACOL>(buf, fa0 + 16 * f, ks, lane);
-                    fb[f] = sim_frag<BCOL>(buf + kSimBytes, fb0 + 16 * f, ks, lane);
+                for (int f = 0; f < F; ++f) {
+                    fa[f] = sim_frag<ACOL>(pa, fa0 % kSim + 16 * f, ks, lane);
+                    fb[f] = sim_frag<BCOL>(pb, fb0 % kSim + 16 * f, ks, lane);
                 }
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+                for (int a = 0; a < F; ++a)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < F; ++b)
                         acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
             }
         }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < F; ++b) {
         const int j = fb0 + 16 * b + (lane & 15);
         if (j >= b_rows) continue;
         size_t dst;
@@ -258,7 +282,7 @@ __global__ __launch_bounds__(256, OP == kOpDw ? 3 : 4) void grouped_small_kernel
             dst = (size_t)row * a_dim;
         }
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < F; ++a) {
             const int col = a0 + fa0 + 16 * a + 4 * (lane >> 4);
             f32x4_t v = acc[a][b];
             typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
@@ -301,12 +325,34 @@ int blocks_bound(const GroupedArgs& g, int B) {
 // every row of an operand is whole 16-byte chunks
 bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
 
+template <int OP, bool WHOLE, int TILE>
+void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
+    const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + TILE - 1) / TILE;
+    const int b_tiles = OP == kOpDw ? g.E * ((g.N + TILE - 1) / TILE) : blocks_bound(g, TILE) * g.splits;
+    grouped_small_kernel<OP, WHOLE, TILE><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+}
+// Rows that are no whole chunks, with enough of them and enough outputs, on 128
+// x 128 tiles: half the loads an output.  us, 64 / 128, T tokens x k over E
+// experts (128 x 128 tiles):
+//   fwd K->N  2048x2/8 2049->4097 [1056] 227/166, 1000x1/1 4095->4097 [264] 123/94,
+//             512x2/8 1025->4097 [264] 43.2/38.4, 1025->2049 [136] 26.3/27.8;
+//             8x2/8 4095->14337 [904, two rows an expert] 176/192
+//   dx  N->K  2048x2/8 4097->2049 [544] 294/203, 512x2/8 1433->4095 [256] 53.7/48.1,
+//             4097->1025 [72] 59/89
+//   dw  N x K 2048x2/8 4097x2049 [4488] 345/223, 4096x2/8 1025x1025 [648] 101/79,
+//             513x513 [200] 32.5/39.1, 512x2/8 1025x1025 [648] 23.2/23.8
+bool wide(const GroupedArgs& g, int op) {
+    if (chunked(g)) return false;
+    const auto tiles = [](int width) { return (long)((width + 2 * kSim - 1) / (2 * kSim)); };
+    if (op == kOpDw) return g.E * tiles(g.N) * tiles(g.K) >= 512;
+    const long experts = g.R < g.E ? g.R : g.E, blocks = tiles(g.R);
+    return g.R >= kSim * experts && tiles(op == kOpFwd ? g.N : g.K) * (blocks > experts ? blocks : experts) >= 256;
+}
 template <int OP>
 void launch_small(const GroupedArgs& g, hipStream_t s) {
-    const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + kSim - 1) / kSim;
-    const int b_tiles = OP == kOpDw ? g.E * ((g.N + kSim - 1) / kSim) : blocks_bound(g, kSim) * g.splits;
-    if (chunked(g)) grouped_small_kernel<OP, true><<<a_tiles * b_tiles, 256, 0, s>>>(g);
-    else grouped_small_kernel<OP, false><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+    if (chunked(g)) launch_small_tiles<OP, true, kSim>(g, s);
+    else if (wide(g, OP)) launch_small_tiles<OP, false, 2 * kSim>(g, s);
+    else launch_small_tiles<OP, false, kSim>(g, s);
 }
 
 }  // namespace

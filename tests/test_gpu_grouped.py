@@ -64,6 +64,9 @@ SHAPES = [
     (1100, 2, 4, 1032, 2056, 64, (1,)),
     (1030, 1, 1, 7304, 1096, 1, ()),
     (1030, 1, 1, 1096, 7304, 1, ()),
+    (700, 2, 2, 65, 4100, 1, ()),            # odd widths, many outputs
+    (700, 2, 2, 4100, 65, 16, ()),
+    (300, 2, 4, 1030, 2051, 64, (2,)),
 ]
 
 
