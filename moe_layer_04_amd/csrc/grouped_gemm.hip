@@ -13,6 +13,8 @@
 #include "grouped.hpp"
 #include "tiles.hpp"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -103,6 +105,54 @@ __device__ __forceinline__ bf16x8_t sim_frag(const char* buf, int first, int ks,
         return bf16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     } else {
         return *reinterpret_cast<const bf16x8_t*>(buf + sim_at<false>(first + (lane & 15), ks * 4 + (lane >> 4)));
+    }
+}
+
+// The tile of a weight gradient, `rows` x `cols` values of it from `first` on,
+// through LDS: a store instruction writes whole rows of the tile, where the
+// accumulators hold 16 rows of four values (16 rows over 8 experts of 1433 x 4095:
+// 32.7 us against 57.4; 4096 rows, 4097 x 2049: 181 against 221).  Chunks of 16 bytes are permuted by the row.
+template <int TILE, bool F32>
+__device__ __forceinline__ void store_grad(char* lds, const f32x4_t (&acc)[TILE / 32][TILE / 32],
+                                           const GroupedArgs& g, size_t first, int rows, int cols,
+                                           int fa0, int fb0) {
+    constexpr int size = F32 ? 4 : 2, per = 16 / size, chunks = TILE / per;
+    const int lane = lane_id();
+    auto at = [](int row, int chunk) { return row * TILE * size + ((chunk ^ (row & 7)) << 4); };
+    __syncthreads();  // the last step's fragments are read
+#pragma unroll
+    for (int b = 0; b < TILE / 32; ++b)
+#pragma unroll
+        for (int a = 0; a < TILE / 32; ++a) {
+            const int row = fb0 + 16 * b + (lane & 15), col = fa0 + 16 * a + 4 * (lane >> 4);
+            const f32x4_t v = acc[a][b];
+            if constexpr (F32)
+                *reinterpret_cast<f32x4_t*>(lds + at(row, col / per)) = v;
+            else
+                *reinterpret_cast<uint2*>(lds + at(row, col / per) + (col & 4) * 2) =
+                    uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+    __syncthreads();
+    typedef typename std::conditional<F32, f32x4_t, u16x8_t>::type chunk_t;
+    typedef typename std::conditional<F32, float, uint16_t>::type value_t;
+    typedef chunk_t any_t __attribute__((aligned(size)));
+#pragma unroll 4
+    for (int i = (int)threadIdx.x; i < TILE * chunks; i += 256) {
+        const int row = i / chunks, c = i % chunks;
+        if (row >= rows || c * per >= cols) continue;
+        chunk_t v = *reinterpret_cast<const chunk_t*>(lds + at(row, c));
+        value_t* o = (value_t*)g.out + first + (size_t)row * g.K + c * per;
+        if (c * per + per <= cols) {
+            any_t* p = reinterpret_cast<any_t*>(o);
+            if constexpr (F32) {
+                if (g.accumulate) v += *p;
+            }
+            *p = v;
+        } else {
+#pragma unroll
+            for (int j = 0; j < per - 1; ++j)
+                if (c * per + j < cols) o[j] = F32 && g.accumulate ? o[j] + v[j] : v[j];
+        }
     }
 }
 
@@ -266,43 +316,33 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
             }
         }
     }
+    if constexpr (OP == kOpDw) {
+        const size_t at = ((size_t)e * g.N + b0) * g.K + a0;
+        const int cols = min(g.K - a0, TILE);
+        if (g.out_f32) store_grad<TILE, true>(lds[0], acc, g, at, b_rows, cols, fa0, fb0);
+        else store_grad<TILE, false>(lds[0], acc, g, at, b_rows, cols, fa0, fb0);
+        return;
+    }
 #pragma unroll
     for (int b = 0; b < F; ++b) {
         const int j = fb0 + 16 * b + (lane & 15);
         if (j >= b_rows) continue;
-        size_t dst;
-        if constexpr (OP == kOpDw) {
-            dst = ((size_t)e * g.N + b0 + j) * g.K;
-        } else {
-            int row = row0 + j;
-            if (g.splits == 1 && g.how_out == kRowSlot) {
-                row = grouped_row(g, row, kRowSlot);
-                if (row < 0) continue;
-            }
-            dst = (size_t)row * a_dim;
+        int row = row0 + j;
+        if (g.splits == 1 && g.how_out == kRowSlot) {
+            row = grouped_row(g, row, kRowSlot);
+            if (row < 0) continue;
         }
 #pragma unroll
         for (int a = 0; a < F; ++a) {
             const int col = a0 + fa0 + 16 * a + 4 * (lane >> 4);
             f32x4_t v = acc[a][b];
-            typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
             typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
-            if (OP != kOpDw && g.splits > 1) {
+            if (g.splits > 1) {
                 if (col < a_dim)
                     *reinterpret_cast<f32x4_t*>((float*)g.out + ((size_t)sp * g.R + row0 + j) *
                                                 grouped_part_ld(a_dim) + col) = v;
-            } else if (OP == kOpDw && g.out_f32) {
-                float* o = (float*)g.out + dst + col;
-                if (col + 4 <= a_dim) {
-                    f32x4_any_t* p = reinterpret_cast<f32x4_any_t*>(o);
-                    *p = g.accumulate ? *p + v : v;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        if (col + i < a_dim) o[i] = g.accumulate ? o[i] + v[i] : v[i];
-                }
             } else {
-                uint16_t* o = (uint16_t*)g.out + dst + col;
+                uint16_t* o = (uint16_t*)g.out + (size_t)row * a_dim + col;
                 u16x4_t q;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) q[i] = f32_to_bf16_bits(v[i]);
@@ -480,27 +520,37 @@ void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
     launch_rows<true>(g, workspace, s);
 }
 
-// The weight gradient on small tiles: up to ten a CU, while the rows of an
-// expert are few (a full tile's start costs more than its steps there).  us,
-// small / full tiles, rows over E experts of N x K (small tiles): 666/8 1032x256
-// [544] 9.4/15.6, 300/2 1024x1024 [512] 9.3/15.6, 64/8 1024x1024 [2048]
-// 10.2/11.3, 1024/8 the same 14.7/15.2, 19/38 2056x128 [2508] 10.2/31.7; 180/23
-// 640x768 [2760] 11.3/13.7, 1024/8 2048x1024 [4096] 34/16, 512/64 2048x512
-// [16384] 47/27; 16625/41 120x1728 [2214] 37.7/32.6.
+// The weight gradient on small or on full tiles, by an estimate of what they
+// take in 1/20 us a CU: 11 a step of a small tile (with its share of a CU's four)
+// and 3 to store it; 29 a step of a full tile, 64 to store it and 100 to start.
+// us, small / full, rows over E experts of N x K (small tiles, steps):
+//   1024/8 1024x1024 [2048, 2] 13.5/14.4    2048/8 the same [4] 22.2/17.2
+//   4096/8 1024x256 [512, 8] 14.7/21.0      8192/8 the same [16] 26.2/29.2
+//   16384/8 the same [32] 47.4/32.5         512/8 2048x1024 [4096, 1] 20.0/13.1
+//   256/8 4096x4096 [32768, 1] 88.5/57.5    19/38 2056x128 [2508, 1] 10.0/21.4
+//   54/73 64x5696 [6497, 1] 17.9/35.3       488/245 576x192 [6615, 1] 21.2/29.7
+//   4096/1 512x512 [64, 64] 47.2/24.0       7448/12 128x3032 [1152, 10] 30.8/22.3
 static bool small_dw(const GroupedArgs& g) {
-    if (!chunked(g)) return true;
-    const long tiles = (long)((g.K + kSim - 1) / kSim) * ((g.N + kSim - 1) / kSim) * g.E;
-    return tiles <= 2560 && g.R <= 256L * (g.R < g.E ? g.R : g.E);
+    if (!chunked(g) || g.R == 0) return true;
+    const long experts = g.R < g.E ? g.R : g.E, steps = (g.R / experts + kSim - 1) / kSim;
+    auto tiles = [&](int side) { return (long)((g.K + side - 1) / side) * ((g.N + side - 1) / side) * g.E; };
+    const long small = tiles(kSim) > 256 ? tiles(kSim) : 256;
+    const int splits = grouped_tiles_dw_splits(g);
+    const long rounds = (tiles(256) * splits + 255) / 256, part = (steps + splits - 1) / splits;
+    return small * (11 * steps + 3) <= 256 * (rounds * (29 * part + 64) + 100);
 }
 size_t grouped_dw_workspace(const GroupedArgs& g) {
-    const int splits = small_dw(g) || g.R == 0 ? 1 : grouped_tiles_dw_splits(g);
+    const int splits = small_dw(g) ? 1 : grouped_tiles_dw_splits(g);
     return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;
 }
 void launch_grouped_dw(const GroupedArgs& call, void* workspace, hipStream_t s) {
     GroupedArgs g = call;
-    g.splits = small_dw(g) || g.R == 0 ? 1 : grouped_tiles_dw_splits(g);
-    if (small_dw(g)) launch_small<kOpDw>(g, s);
-    else launch_grouped_tiles_dw(g, workspace, s);
+    if (small_dw(g)) {
+        launch_small<kOpDw>(g, s);
+    } else {
+        g.splits = grouped_tiles_dw_splits(g);
+        launch_grouped_tiles_dw(g, workspace, s);
+    }
 }
 
 }  // namespace moe

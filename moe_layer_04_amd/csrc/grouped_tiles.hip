@@ -463,8 +463,10 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
 //
 // Tile order: each XCD takes an eighth of every expert's tiles (experts have
 // different numbers of rows; an expert to an XCD would leave most of them
-// idle), the eighths turned by one from expert to expert so that few tiles
-// spread too; within it kGroup column tiles fastest, then the n tiles.
+// idle), the eighths turned from expert to expert so that few tiles spread too
+// -- not by one each, as a workgroup's tiles lie a multiple of eight experts
+// apart when there are few (488 rows over 245 experts of 576 x 192: 59.0 us by
+// one, 29.7 as here); within it kGroup column tiles fastest, then the n tiles.
 // Few output tiles over many rows: an expert's rows are cut into g.splits ranges
 // of whole steps, each a "part" e * splits + s with its own fp32 product in the
 // workspace; dw_join adds them up in order.  (1024 x 1024 over 8192 rows of one
@@ -504,7 +506,7 @@ struct DwWalk {
         DwTile t = {0, 0, 0, 0, 0};
         for (; at < end; at += stride) {
             t.e = at / per_xcd;
-            const int i = ((xcd + t.e) % 8) * per_xcd + at % per_xcd;
+            const int i = ((xcd + t.e + t.e / 8 + t.e / 32) % 8) * per_xcd + at % per_xcd;
             if (i >= tiles) continue;
             dw_rows<PARTS>(g, t.e, t.row0, t.rows);
             if (rows_only && t.rows == 0) continue;
@@ -640,14 +642,20 @@ __device__ __forceinline__ void store_dw(char* st, const f32x16_t (&acc)[4][2],
     }
 }
 
-// the same rows and columns as zeros, without LDS
-__device__ __forceinline__ void store_dw_zeros(const GroupedArgs& g, int e, int n0, int k0) {
-    const int lane = late_lane(), size = g.out_f32 ? 4 : 2;
+// the same rows and columns as zeros, without LDS; `zeros`: accumulators of no steps
+__device__ __forceinline__ void store_dw_zeros(const f32x16_t& zeros, const GroupedArgs& g, int e,
+                                               int n0, int k0) {
+    const int lane = late_lane(), size = g.out_f32 ? 4 : 2, lg = g.out_f32 ? 5 : 4;  // 2^lg chunks a row
+    const uint32_t ld = (uint32_t)(g.K * size);
     char* base = (char*)g.out + (((size_t)e * g.N + n0) * g.K + k0) * size;
-    const int words = min(128, g.K - k0) * size / 4, rows = min(64, g.N - n0);
-    for (int row = 0; row < rows; ++row)
-        for (int i = lane; i < words; i += kWave)
-            reinterpret_cast<float*>(base + (size_t)row * g.K * size)[i] = 0.0f;
+    const prsrc_t r = pmake_rsrc(base, (uint32_t)min(64, g.N - n0) * ld - (uint32_t)(k0 * size));
+    const uint32_t c = (uint32_t)(lane & ((1 << lg) - 1)) * 16;
+    // rows past the last are out of range
+    uint32_t at = c < (uint32_t)(min(128, g.K - k0) * size) ? (uint32_t)(lane >> lg) * ld + c : kNowhere;
+    const i32x4_t z = __builtin_bit_cast(i32x4_t, f32x4_t{zeros[0], zeros[1], zeros[2], zeros[3]});
+#pragma unroll 1
+    for (int i = 0; i < 1 << lg; ++i, at += (uint32_t)(kWave >> lg) * ld)
+        __builtin_amdgcn_raw_buffer_store_b128(z, r, at, 0, 0);
 }
 
 template <bool LOOK, DwOut OUT>
@@ -819,8 +827,8 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(GroupedArgs g) {
             early = true;
         }
         if (used) {
-            if (t.rows == 0) {
-                store_dw_zeros(g, t.e, t.b0 + brow0, t.a0 + arow0);
+            if (OUT != DwOut::kF32Add && t.rows == 0) {  // (kF32Add walks tiles with rows only)
+                store_dw_zeros(acc[0][0], g, t.e, t.b0 + brow0, t.a0 + arow0);
             } else {
                 store_dw<OUT>(slot_a(asl == 0 ? 2 : asl - 1) + gw * (kSlotBytes / 4), acc, g, t.e,
                               t.b0 + brow0, t.a0 + arow0);

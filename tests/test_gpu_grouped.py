@@ -67,6 +67,9 @@ SHAPES = [
     (700, 2, 2, 65, 4100, 1, ()),            # odd widths, many outputs
     (700, 2, 2, 4100, 65, 16, ()),
     (300, 2, 4, 1030, 2051, 64, (2,)),
+    (12000, 1, 3, 136, 72, 64, (1,)),        # dw in ranges, padded, an expert without rows
+    (90, 2, 40, 520, 264, 1, (7,)),          # dw: few full tiles of many experts
+    (500, 2, 60, 520, 776, 16, (7,)),
 ]
 
 
