@@ -168,12 +168,23 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int a_dim = OP == kOpFwd ? g.N : g.K;
     const int a_tiles = (a_dim + TILE - 1) / TILE;
-    const int a0 = ((int)blockIdx.x % a_tiles) * TILE;  // first output column
-    int bt = (int)blockIdx.x / a_tiles, sp = 0;
+    int tile = (int)blockIdx.x;
+    // Where rows of the output (and of dx's weights) are no whole lines of 128
+    // bytes, neighbouring tiles share lines: they go to one XCD (workgroup g runs
+    // on XCD g % 8), whose L2 joins them.  dw, us: 4 rows over 99 experts of 8768
+    // x 1042 in fp32 1409 apart, 572 so; dx 8x2/8 14337 -> 4095 220, 198; whole
+    // lines, dw 1024/8 1024 x 1024: 13.6, 14.6; fwd 64x2/8 4095 -> 14337: 228, 257.
+    if (OP != kOpFwd && (uint32_t)a_dim * (OP == kOpDw && g.out_f32 ? 4 : 2) % 128 != 0) {
+        const int per_xcd = (int)gridDim.x / 8;
+        tile = tile % 8 * per_xcd + tile / 8;
+    }
+    const int a0 = (tile % a_tiles) * TILE;  // first output column
+    int bt = tile / a_tiles, sp = 0;
     int e, row0, rows, b0 = 0, red;
     if constexpr (OP == kOpDw) {
         const int n_tiles = (g.N + TILE - 1) / TILE;
         e = bt / n_tiles;
+        if (e >= g.E) return;  // the grid is rounded up
         b0 = (bt % n_tiles) * TILE;
         row0 = grouped_offset_scalar(g, e);
         rows = max(grouped_offset_scalar(g, e + 1) - row0, 0);
@@ -369,7 +380,7 @@ template <int OP, bool WHOLE, int TILE>
 void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
     const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + TILE - 1) / TILE;
     const int b_tiles = OP == kOpDw ? g.E * ((g.N + TILE - 1) / TILE) : blocks_bound(g, TILE) * g.splits;
-    grouped_small_kernel<OP, WHOLE, TILE><<<a_tiles * b_tiles, 256, 0, s>>>(g);
+    grouped_small_kernel<OP, WHOLE, TILE><<<(a_tiles * b_tiles + 7) / 8 * 8, 256, 0, s>>>(g);
 }
 // Rows that are no whole chunks, with enough of them and enough outputs, on 128
 // x 128 tiles: half the loads an output.  us, 64 / 128, T tokens x k over E
