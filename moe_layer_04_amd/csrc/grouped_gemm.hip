@@ -462,7 +462,7 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const float* __restrict_
 // Ranges of full tiles while a CU has no more than one and a range 16 steps:
 // 1024x1/1 14336->1024 214 whole, 68.6 in four, 46.3 in eight; 4096->4096 67.1,
 // 51.4, 49.2 (two, four); two ranges of 8 steps 1024->4096 23.3, 29.6.  Of small
-// tiles while a CU has no more than two, a range eight steps and the whole 32:
+// tiles up to 2.5 a CU, while a range has eight steps and the whole 32:
 // 1024x1/1 4096->512 34.9 whole, 18.7 in four, 21.1 in eight; 2048->512 19.4,
 // 13.7, 16.1; 1024->512 9.8, 13.4 (four).
 struct RowsPlan {
@@ -490,7 +490,7 @@ RowsPlan rows_plan(const GroupedArgs& g, bool dx) {
         least = 16;
     } else {
         work = small;
-        most = 512;
+        most = 640;
         least = steps < 32 ? steps : 8;
     }
     while (p.splits < 16 && work * p.splits * 2 <= most && steps / (p.splits * 2) >= least) p.splits *= 2;
