@@ -461,7 +461,7 @@ typedef enum {
  * topk < 1, unknown bits in `rows`, bits without sorted_ids, an unknown `out`;
  * UNSUPPORTED for E > 256, topk > 16, R or T*topk >= 2^28, K or N >= 2^20,
  * N*K*2 >= 2^31 (one expert's weights), a gathered operand of 2^31 bytes or
- * more, or more than 2^31 output tiles of 64 x 64; WORKSPACE.
+ * more, or 2^24 - 8 output tiles of 64 x 64 or more; WORKSPACE.
  */
 moe_status moe_grouped_gemm(const void *x, const void *w, const int32_t *expert_offsets,
                             const int32_t *sorted_ids, int rows, int T, int topk, int R, int E,
@@ -496,7 +496,7 @@ moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *exp
  * Padding rows are written as zeros.  a and dg must not overlap an input.
  * Errors: INVALID_ARG for null or misaligned pointers, negative sizes, fewer slots than rows without
  * sorted_ids, dtopk_weights without topk_weights; UNSUPPORTED for R or slots
- * >= 2^28 or N >= 2^20.
+ * >= 2^28, N >= 2^20 or R * max(ceil(N/8), 256) > 2^32 - 256.
  */
 moe_status moe_silu_mul(const void *g, const float *topk_weights, const int32_t *sorted_ids,
                         const int32_t *num_rows, int slots, int R, int N, void *a, void *stream);
@@ -531,7 +531,8 @@ moe_status moe_silu_mul_bwd(const void *da, const void *g, const float *topk_wei
  *
  * Errors: INVALID_ARG for null or misaligned pointers, negative sizes,
  * eps <= 0, a bad h_dtype, or a combination other than those above;
- * UNSUPPORTED for K >= 2^20, topk > 16 or M*topk >= 2^28; WORKSPACE.
+ * UNSUPPORTED for K >= 2^20, topk > 16, M >= 2^22 or M*topk >= 2^28;
+ * WORKSPACE.
  */
 moe_status moe_block_norm(const void *h, const void *o, const float *gate, const float *w_post,
                           const float *w_pre, int h_dtype, int M, int K, int topk, float res_scale,

@@ -15,6 +15,7 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr long kMaxRows = 1L << 28;     // sorted rows, slots
 constexpr int kMaxWidth = 1 << 20;      // K, N
+constexpr long kMaxThreads = 1L << 32;  // of a launch
 constexpr long kMaxGather = 1L << 31;   // bytes of a gathered operand, of one expert's weights
 
 bool misaligned(const void* p) { return p && ((uintptr_t)p & 15u); }
@@ -53,9 +54,9 @@ moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int3
     if (E > MOE_MAX_EXPERTS || topk > MOE_MAX_TOPK || R >= kMaxRows || slots >= kMaxRows ||
         K >= kMaxWidth || N >= kMaxWidth || (long)N * K * 2 >= kMaxGather)
         return MOE_ERR_UNSUPPORTED;
-    // one-dimensional grids of 64 x 64 output tiles
-    const long wide = ((K > N ? K : N) + 63) / 64;
-    if (wide * (R / 64 + (long)E) >= (1L << 31) || (long)E * ((K + 63) / 64) * ((N + 63) / 64) >= (1L << 31))
+    // a launch of 64 x 64 output tiles, 256 threads each, rounded up to eight tiles
+    const long wide = ((K > N ? K : N) + 63) / 64, most = kMaxThreads / 256 - 8;
+    if (wide * (R / 64 + (long)E) >= most || (long)E * ((K + 63) / 64) * ((N + 63) / 64) >= most)
         return MOE_ERR_UNSUPPORTED;
     g->w = g->x = g->dy = nullptr;
     g->offsets = offsets;
@@ -171,8 +172,9 @@ static moe_status gated_check(moe::GatedArgs* a, const void* g, const float* top
                               int N) {
     if (slots < 0 || R < 0 || N < 1) return MOE_ERR_INVALID_ARG;
     if (R >= kMaxRows || slots >= kMaxRows || N >= kMaxWidth) return MOE_ERR_UNSUPPORTED;
-    // a thread per 8 values, 256 a workgroup, in a one-dimensional grid
-    if ((long)R * ((N + 7) / 8) >= 256L << 31) return MOE_ERR_UNSUPPORTED;
+    // a thread per 8 values, or a workgroup of 256 a row
+    const long row = (N + 7) / 8;
+    if ((long)R * (row > 256 ? row : 256) > kMaxThreads - 256) return MOE_ERR_UNSUPPORTED;
     // without sorted_ids row i is slot i
     if (topk_weights && !sorted_ids && slots < R) return MOE_ERR_INVALID_ARG;
     if (misaligned(g) || misaligned(topk_weights) || misaligned(sorted_ids) ||
@@ -230,6 +232,7 @@ static moe_status norm_sizes(int h_dtype, int M, int K, int topk, int du_topk) {
     if (M < 0 || K < 1 || topk < 1 || du_topk < 1) return MOE_ERR_INVALID_ARG;
     if (K >= kMaxWidth || topk > MOE_MAX_TOPK || du_topk > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
     if ((long)M * topk >= kMaxRows || (long)M * du_topk >= kMaxRows) return MOE_ERR_UNSUPPORTED;
+    if (M * 1024L >= kMaxThreads) return MOE_ERR_UNSUPPORTED;  // a workgroup a row
     return MOE_OK;
 }
 

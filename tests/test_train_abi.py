@@ -40,7 +40,8 @@ def test_grouped_rows_refusals(lib, name):
     for kw in (dict(E=257), dict(topk=17), dict(R=1 << 28), dict(T=1 << 27), dict(K=1 << 20),
                dict(N=1 << 20), dict(K=1 << 15, N=1 << 15),      # one expert's weights: 2 GiB
                dict(T=1 << 24, K=64, N=64),                       # the gathered rows: 2 GiB
-               dict(R=(1 << 28) - 1, K=1 << 19, N=64, T=8, rows=0)):   # the grid
+               dict(R=(1 << 28) - 1, K=1 << 19, N=64, T=8, rows=0),    # the grid
+               dict(R=1 << 22, K=1 << 14, N=1 << 14, T=8, rows=0)):    # its threads
         assert call(**kw) == UNS, kw
     assert call(R=0, a=None, w=None, off=None, ids=None, out=None, rows=0) == OK
     query = dict(a=None, w=None, off=None, ids=None, out=None, ws=None)
@@ -103,7 +104,8 @@ def test_silu_mul_refusals(lib):
                    dict(wt=MISALIGNED), dict(ids=MISALIGNED), dict(nr=MISALIGNED),
                    dict(ids=None, slots=15)):
             assert call(**kw) == INV, kw
-        for kw in (dict(R=1 << 28), dict(slots=1 << 28), dict(N=1 << 20)):
+        for kw in (dict(R=1 << 28), dict(slots=1 << 28), dict(N=1 << 20),
+                   dict(R=1 << 24, slots=1 << 24), dict(R=1 << 20, slots=1 << 20, N=1 << 15)):
             assert call(**kw) == UNS, kw
         assert call(R=0, g=None) == OK
     assert fwd(a=None) == INV and fwd(a=MISALIGNED) == INV
@@ -127,7 +129,7 @@ def test_block_norm_refusals(lib):
                dict(h=MISALIGNED), dict(o=MISALIGNED), dict(gate=MISALIGNED),
                dict(wp=MISALIGNED), dict(ho=MISALIGNED), dict(u=MISALIGNED), dict(r1=MISALIGNED)):
         assert call(**kw) == INV, kw
-    for kw in (dict(K=1 << 20), dict(topk=17), dict(M=1 << 27)):
+    for kw in (dict(K=1 << 20), dict(topk=17), dict(M=1 << 27), dict(M=1 << 22)):
         assert call(**kw) == UNS, kw
     assert call(M=0, h=None) == OK
 
@@ -154,7 +156,7 @@ def test_block_norm_bwd_refusals(lib):
                dict(dh=at["dho"]), dict(dh=at["ho"]), dict(do=at["o"]), dict(do=at["du"]),
                dict(ws=ctypes.c_void_p(0x10010)), dict(dho=0x10004), dict(dwn=0x10004)):
         assert call(**kw) == INV, kw
-    for kw in (dict(K=1 << 20), dict(topk=17), dict(dtopk=17), dict(M=1 << 27)):
+    for kw in (dict(K=1 << 20), dict(topk=17), dict(dtopk=17), dict(M=1 << 27), dict(M=1 << 22)):
         assert call(**kw) == UNS, kw
     assert lib.moe_block_norm_bwd(*[FAKE] * 9, 0, 4, 64, 2, 2, 1.0, *[FAKE] * 5, FAKE, None,
                                   None) == INV
