@@ -494,9 +494,9 @@ moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *exp
  *                  they are
  *
  * Padding rows are written as zeros.  a and dg must not overlap an input.
- * Errors: INVALID_ARG for null or misaligned pointers, negative sizes, fewer slots than rows without
- * sorted_ids, dtopk_weights without topk_weights; UNSUPPORTED for R or slots
- * >= 2^28, N >= 2^20 or R * max(ceil(N/8), 256) > 2^32 - 256.
+ * Errors: INVALID_ARG for null or misaligned pointers, negative sizes, fewer
+ * slots than rows without sorted_ids, dtopk_weights without topk_weights;
+ * UNSUPPORTED for R or slots >= 2^28, N >= 2^20 or R * max(ceil(N/8), 256) > 2^32 - 256.
  */
 moe_status moe_silu_mul(const void *g, const float *topk_weights, const int32_t *sorted_ids,
                         const int32_t *num_rows, int slots, int R, int N, void *a, void *stream);
