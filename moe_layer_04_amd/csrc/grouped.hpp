@@ -78,12 +78,14 @@ __device__ __forceinline__ GroupedScan grouped_scan(const GroupedArgs& g, int B)
         s.nb[j] = (int)(((uint32_t)c + (uint32_t)B - 1) / (uint32_t)B);
         sum += s.nb[j];
     }
+    // inclusive sum over the wave: within rows of 16 lanes, then the rows' ends on
     int incl = sum;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int v = __shfl_up(incl, d);
-        if (lane >= d) incl += v;
-    }
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xf, 0xf, false);  // row_shr:1
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xf, 0xf, false);  // row_shr:2
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xf, 0xf, false);  // row_shr:4
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xf, 0xf, false);  // row_shr:8
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xa, 0xf, false);  // row_bcast:15 to rows 1, 3
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xc, 0xf, false);  // row_bcast:31 to rows 2, 3
     // ascending offsets never reach the bound, which the launch grids cover
     s.total = min(__builtin_amdgcn_readlane(incl, kWave - 1), g.R / B + min(g.R, g.E));
     s.start = incl - sum;

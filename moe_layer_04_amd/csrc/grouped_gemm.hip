@@ -111,7 +111,8 @@ __device__ __forceinline__ bf16x8_t sim_frag(const char* buf, int first, int ks,
 // The tile of a weight gradient, `rows` x `cols` values of it from `first` on,
 // through LDS: a store instruction writes whole rows of the tile, where the
 // accumulators hold 16 rows of four values (16 rows over 8 experts of 1433 x 4095:
-// 32.7 us against 57.4; 4096 rows, 4097 x 2049: 181 against 221).  Chunks of 16 bytes are permuted by the row.
+// 32.7 us against 57.4; 4096 rows, 4097 x 2049: 181 against 221).  Chunks of 16
+// bytes are permuted by the row.
 template <int TILE, bool F32>
 __device__ __forceinline__ void store_grad(char* lds, const f32x4_t (&acc)[TILE / 32][TILE / 32],
                                            const GroupedArgs& g, size_t first, int rows, int cols,
