@@ -459,6 +459,13 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const float* __restrict_
 //                 1024->1024 28.5/25.4,   4096->1024 85.1/53.7
 //       37x8/8    14336->512 33.9/33.3,   14336->1024 49.2/44.0, 14336->2048 102/93
 //       8x2/8     28672->4096 313/269;    8192x2/8 512->256 19.2/16.5
+// but small ones for short reductions of experts with few rows, where a full
+// tile is mostly its start and end:
+//   fwd 160x8/128 64->4096 22.7/43.0, 192->8192 85/130, 512->4096 98/118,
+//                 2048->2048 223/188;  640x8/128 512->4096 119/131;
+//       1280x8/128 64->4096 56.1/51.3, 512->4096 174/145
+//   dx  128x8/128 64->4096 24.8/43.8, 192->8192 92/124, 512->4096 110/127,
+//                 1024->2048 110/104;  640x8/128 512->4096 136/136
 //
 // Ranges of full tiles while a CU has no more than one and a range 16 steps:
 // 1024x1/1 14336->1024 214 whole, 68.6 in four, 46.3 in eight; 4096->4096 67.1,
@@ -479,7 +486,9 @@ RowsPlan rows_plan(const GroupedArgs& g, bool dx) {
     const long full = (long)((cols + 255) / 256) * (full_blocks > experts ? full_blocks : experts);
     RowsPlan p = {RowsPlan::kSmall, 1};
     if (chunked(g) && !dx && g.R <= 3 * experts) p.on = RowsPlan::kStream;
-    else if (chunked(g) && (small > 512 || small * steps >= 512 * 64)) p.on = RowsPlan::kFull;
+    else if (chunked(g) && (small > 512 || small * steps >= 512 * 64) &&
+             (steps > 8 || g.R > 48 * experts))
+        p.on = RowsPlan::kFull;
     long work, most, least;  // workgroups whole, the most of them, a range's least steps
     if (p.on == RowsPlan::kStream) {
         work = (long)((cols + 31) / 32) * experts;
