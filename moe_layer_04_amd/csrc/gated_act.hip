@@ -9,7 +9,9 @@
 // p = sorted[i] is the row's slot.  Rows hold the gate half, then the up
 // half.  Both passes are bound by HBM: every value is read and written once, 16
 // bytes a lane; arithmetic and the row's dot product are fp32.
-// 8192 x 14336: backward 221 us (5.3 TB/s); 16 x 14336: forward 2.7 us, a launch.
+// 8192 x 14336: backward 211 us (5.6 TB/s), forward 106 us (6.6 TB/s), by loads and
+// stores that keep nothing in the L2 (219 and 117 us by ordinary ones); 16 x
+// 14336: forward 2.7 us, a launch.
 #include "common.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
@@ -44,12 +46,12 @@ __global__ __launch_bounds__(256) void silu_mul_kernel(GatedArgs a) {
     if (p >= 0) {
         const float w = a.weights ? a.weights[p] : 1.0f;
         float z[V], u[V];
-        ld_bf16<ANY>(g, n, z);
-        ld_bf16<ANY>(g + a.N, n, u);
+        ld_bf16<ANY, true>(g, n, z);
+        ld_bf16<ANY, true>(g + a.N, n, u);
 #pragma unroll
         for (int v = 0; v < V; ++v) y[v] = w * silu(z[v]) * u[v];
     }
-    st_bf16<ANY>(a.out + (size_t)i * a.N + col, n, y);
+    st_bf16<ANY, true>(a.out + (size_t)i * a.N + col, n, y);
 }
 
 // a workgroup per row
@@ -69,9 +71,9 @@ __global__ __launch_bounds__(TH) void silu_mul_bwd_kernel(GatedArgs a) {
         float dg[V] = {}, du[V] = {};
         if (p >= 0) {
             float z[V], u[V], da[V];
-            ld_bf16<ANY>(g + col, n, z);
-            ld_bf16<ANY>(g + a.N + col, n, u);
-            ld_bf16<ANY>(d + col, n, da);
+            ld_bf16<ANY, true>(g + col, n, z);
+            ld_bf16<ANY, true>(g + a.N + col, n, u);
+            ld_bf16<ANY, true>(d + col, n, da);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z[v]));
@@ -81,8 +83,8 @@ __global__ __launch_bounds__(TH) void silu_mul_bwd_kernel(GatedArgs a) {
                 du[v] = da[v] * w * act;
             }
         }
-        st_bf16<ANY>(o + col, n, dg);
-        st_bf16<ANY>(o + a.N + col, n, du);
+        st_bf16<ANY, true>(o + col, n, dg);
+        st_bf16<ANY, true>(o + a.N + col, n, du);
     }
     if (!a.dweights || p < 0) return;  // the same for the whole workgroup
     dot = wave_sum_f32(dot);
