@@ -44,8 +44,8 @@ constexpr int kOpFwd = 0, kOpDx = 1, kOpDw = 2;
 //
 // Bound by the latency of a step, 0.5-0.6 us with up to two workgroups a CU
 // (1024 rows of one expert, 4096 -> 1024: 34.9 us for 64 steps).  406 rows over 7
-// experts of 1001 x 330, dx: 14.2 us for 16 steps; 666 rows over 8 experts, dw
-// of 1032 x 256 in fp32: 7.4 us.
+// experts of 1001 x 330, dx: 11.5 us a call of 16 steps; 666 rows over 8 experts,
+// dw of 1032 x 256 in fp32: 7.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kSim = 64;                       // tile and step
 constexpr int kSimBytes = kSim * kSim * 2;     // one operand's step
@@ -54,23 +54,36 @@ constexpr int kSimAhead = 2;                   // steps loaded ahead
 typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
 
+// What a kernel knows of the widths: multiples of 8, at least 8, or nothing.
+enum class Widths { kWhole, kLong, kAny };
+
+// What chunks outside an operand are loaded from: a branch a chunk costs more (us,
+// with branches / so: 406 rows over 7 experts of 1001 x 330, dx 14.7/11.5; 4096
+// rows over 8 of 4097 x 2049, dw 177/164; but 16 rows over 8 of 14337 x 4095,
+// forward 176/186)
+__device__ const uint16_t kZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+
 // Columns c..c+7 of a row of `width`, zeros past its end and for no row.  A
 // row's last chunk is loaded as the row's last 8 values, so that nothing past
 // the row is read, and moved into place by settle_chunk when it is stored (a
 // move here would wait for the load).
-template <bool WHOLE>  // the width is a multiple of 8
+template <Widths W>
 __device__ __forceinline__ u16x8_t load_chunk(const uint16_t* row, int c, int width) {
-    u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if constexpr (WHOLE) {
-        if (row && c < width) v = *reinterpret_cast<const u16x8_t*>(row + c);
-    } else if (width < 8) {
+    const bool in = row && c < width;
+    if constexpr (W == Widths::kWhole) {
+        typedef const __attribute__((address_space(1))) u16x8_t* global_t;
+        return *(global_t)(uintptr_t)(in ? row + c : kZeros);
+    } else {
+        if (W == Widths::kAny && width < 8) {
+            u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (row && c + i < width) v[i] = row[c + i];
-    } else if (row && c < width) {
-        v = *reinterpret_cast<const u16x8_any_t*>(row + min(c, width - 8));
+            for (int i = 0; i < 7; ++i)
+                if (row && c + i < width) v[i] = row[c + i];
+            return v;
+        }
+        typedef const __attribute__((address_space(1))) u16x8_any_t* global_t;
+        return *(global_t)(uintptr_t)(in ? row + min(c, width - 8) : kZeros);
     }
-    return v;
 }
 __device__ __forceinline__ u16x8_t settle_chunk(u16x8_t v, int c, int width) {
     const int by = width < 8 ? 0 : max(c - (width - 8), 0);  // elements to drop in front (0..7)
@@ -157,7 +170,7 @@ __device__ __forceinline__ void store_grad(char* lds, const f32x4_t (&acc)[TILE 
     }
 }
 
-template <int OP, bool WHOLE, int TILE>
+template <int OP, Widths W, int TILE>
 __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void grouped_small_kernel(
     GroupedArgs g) {
     constexpr bool ACOL = OP != kOpFwd, BCOL = OP == kOpDw;
@@ -242,20 +255,20 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int x = rx[h & 1], y = ry[h & 1];
-                s.a[h] = load_chunk<WHOLE>(x < 0 ? nullptr : g.x + (size_t)x * g.K, a0 + col_at(h), g.K);
-                s.b[h] = load_chunk<WHOLE>(y < 0 ? nullptr : g.dy + (size_t)y * g.N, b0 + col_at(h), g.N);
+                s.a[h] = load_chunk<W>(x < 0 ? nullptr : g.x + (size_t)x * g.K, a0 + col_at(h), g.K);
+                s.b[h] = load_chunk<W>(y < 0 ? nullptr : g.dy + (size_t)y * g.N, b0 + col_at(h), g.N);
             }
         } else {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 if constexpr (OP == kOpFwd) {
                     const int n = a0 + r + 32 * h;
-                    s.a[h] = load_chunk<WHOLE>(n < g.N ? w + (size_t)n * g.K : nullptr, r0 + c * 8, red);
+                    s.a[h] = load_chunk<W>(n < g.N ? w + (size_t)n * g.K : nullptr, r0 + c * 8, red);
                 } else {
                     const int n = r0 + col_row(h);
-                    s.a[h] = load_chunk<WHOLE>(n < red ? w + (size_t)n * g.K : nullptr, a0 + col_at(h), g.K);
+                    s.a[h] = load_chunk<W>(n < red ? w + (size_t)n * g.K : nullptr, a0 + col_at(h), g.K);
                 }
-                s.b[h] = load_chunk<WHOLE>(brow[h], r0 + c * 8, red);
+                s.b[h] = load_chunk<W>(brow[h], r0 + c * 8, red);
             }
         }
         return s;
@@ -264,7 +277,7 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
     // of a reduction that runs along the rows
     const bool a_ends = ACOL && a0 + TILE > g.K, b_ends = BCOL && b0 + TILE > g.N;
     auto settle = [&](Step& s, int step) {
-        if constexpr (WHOLE) return;
+        if constexpr (W == Widths::kWhole) return;
         const int r0 = step * kSim;
         if (a_ends || (!ACOL && r0 + kSim > red)) {
 #pragma unroll
@@ -377,11 +390,11 @@ int blocks_bound(const GroupedArgs& g, int B) {
 // every row of an operand is whole 16-byte chunks
 bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
 
-template <int OP, bool WHOLE, int TILE>
+template <int OP, Widths W, int TILE>
 void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
     const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + TILE - 1) / TILE;
     const int b_tiles = OP == kOpDw ? g.E * ((g.N + TILE - 1) / TILE) : blocks_bound(g, TILE) * g.splits;
-    grouped_small_kernel<OP, WHOLE, TILE><<<(a_tiles * b_tiles + 7) / 8 * 8, 256, 0, s>>>(g);
+    grouped_small_kernel<OP, W, TILE><<<(a_tiles * b_tiles + 7) / 8 * 8, 256, 0, s>>>(g);
 }
 // Rows that are no whole chunks, with enough of them and enough outputs, on 128
 // x 128 tiles: half the loads an output.  us, 64 / 128, T tokens x k over E
@@ -402,9 +415,10 @@ bool wide(const GroupedArgs& g, int op) {
 }
 template <int OP>
 void launch_small(const GroupedArgs& g, hipStream_t s) {
-    if (chunked(g)) launch_small_tiles<OP, true, kSim>(g, s);
-    else if (wide(g, OP)) launch_small_tiles<OP, false, 2 * kSim>(g, s);
-    else launch_small_tiles<OP, false, kSim>(g, s);
+    if (chunked(g)) launch_small_tiles<OP, Widths::kWhole, kSim>(g, s);
+    else if (g.K < 8 || g.N < 8) launch_small_tiles<OP, Widths::kAny, kSim>(g, s);
+    else if (wide(g, OP)) launch_small_tiles<OP, Widths::kLong, 2 * kSim>(g, s);
+    else launch_small_tiles<OP, Widths::kLong, kSim>(g, s);
 }
 
 }  // namespace
