@@ -26,18 +26,19 @@ constexpr int kOpFwd = 0, kOpDx = 1, kOpDw = 2;
 // each, 16x16x32 MFMAs), 64 reduction elements a step.  For products with too
 // few outputs for 256 x 256 tiles, where the time is the latency of a step, and
 // for rows that are not whole 16-byte chunks, which the copies of those tiles
-// cannot take; for many outputs of such rows also as 128 x 128 (see wide).  A step's chunks of 8 elements are loaded into registers two
-// steps ahead (16 bytes at any 2-byte address; a row's last chunk element by
-// element, so that nothing past a row is read) and stored to one of two LDS
-// buffers, a barrier a step.
+// cannot take; for many outputs of such rows also as 128 x 128 (see wide).  A
+// step's chunks of 8 elements are loaded into registers two steps ahead (16
+// bytes at any 2-byte address; a row's last chunk as the row's last 8 elements,
+// so that nothing past a row is read) and stored to one of two LDS buffers, a
+// barrier a step.
 //
 // LDS layouts of 64 rows (or of 64 columns; 128 are two such parts), both 64
-// rows of 128 bytes.  Rows along the output (operands that
-// are contiguous in the reduction): 16-byte chunks permuted by the row as in
-// the full tiles, fragments read directly.  Rows along the reduction: fragments
-// come through the transposing read (lane i of 16 gets column i of four rows,
-// that is 32 bytes of each), 32-byte pieces permuted so that the two times four
-// rows of a half-wave's read fall in different banks.
+// rows of 128 bytes.  Rows along the output (operands that are contiguous in
+// the reduction): 16-byte chunks permuted by the row as in the full tiles,
+// fragments read directly.  Rows along the reduction: fragments come through
+// the transposing read (lane i of 16 gets column i of four rows, that is 32
+// bytes of each), 32-byte pieces permuted so that the two times four rows of a
+// half-wave's read fall in different banks.
 //
 // 16x16x32: lane l supplies row l % 16, reduction 8*(l/16)..+8; its
 // accumulators are rows 4*(l/16)+v of column l % 16.
