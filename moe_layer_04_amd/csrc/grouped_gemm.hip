@@ -223,8 +223,11 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
     const int r = tid >> 3, c = tid & 7;
     auto col_row = [&](int h) { return r + 32 * (h & 1); };
     auto col_at = [&](int h) { return (h >> 1) * kSim + c * 8; };
+    const int fa0 = (wave & 1) * (TILE / 2), fb0 = (wave >> 1) * (TILE / 2);
     const uint16_t* brow[H];  // fwd, dx: fixed rows of B
+    uint64_t padding = 0;     // of the wave's rows
     if constexpr (OP != kOpDw) {
+        padding = grouped_padding(g, row0, rows, fb0, TILE / 2);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             brow[h] = nullptr;
@@ -291,7 +294,6 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
                 s.b[h] = settle_chunk(s.b[h], BCOL ? b0 + col_at(h) : r0 + c * 8, BCOL ? g.N : red);
         }
     };
-    const int fa0 = (wave & 1) * (TILE / 2), fb0 = (wave >> 1) * (TILE / 2);
     f32x4_t acc[F][F];
 #pragma unroll
     for (int a = 0; a < F; ++a)
@@ -353,6 +355,7 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
     for (int b = 0; b < F; ++b) {
         const int j = fb0 + 16 * b + (lane & 15);
         if (j >= b_rows) continue;
+        const bool pad = padding >> (16 * b + (lane & 15)) & 1;
         int row = row0 + j;
         if (g.splits == 1 && g.how_out == kRowSlot) {
             row = grouped_row(g, row, kRowSlot);
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
 #pragma unroll
         for (int a = 0; a < F; ++a) {
             const int col = a0 + fa0 + 16 * a + 4 * (lane >> 4);
-            f32x4_t v = acc[a][b];
+            const f32x4_t v = pad ? f32x4_t{0, 0, 0, 0} : acc[a][b];
             typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
             if (g.splits > 1) {
                 if (col < a_dim)

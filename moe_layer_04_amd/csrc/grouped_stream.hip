@@ -128,6 +128,7 @@ __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs
 #pragma unroll
             for (int w = 0; w < kWaves - 1; ++w) v += part[w][a][lane];
         }
+        if (xoff == kNowhere) v = f32x4_t{0, 0, 0, 0};  // a padding row, whatever W holds
         const int n = a0 + 16 * a + 4 * q;
         if (n >= g.N) continue;  // N is a multiple of 8
         if (g.splits > 1)

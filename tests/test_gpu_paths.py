@@ -1,0 +1,79 @@
+"""The grouped products on every path that computes them: properties that must
+hold whichever kernel runs."""
+import pytest
+import torch
+
+from tests._train_ref import bf16, routing
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import moe_layer_04_amd as m
+    m.load_library()
+    return m
+
+
+def note(msg):
+    print(f"[gpu-test] {msg}", flush=True)
+
+
+# One shape a path of the rows products: T, topk, E, block_m, the reduction's
+# length, the output's width; every expert's range ends in padding rows.
+ROWS = {
+    "stream": (4, 2, 8, 2, 200, 40),
+    "stream, quarters": (4, 2, 8, 2, 1032, 72),
+    "stream, ranges": (4, 2, 8, 2, 8200, 40),
+    "small": (101, 2, 3, 16, 72, 136),
+    "small, ranges": (101, 2, 3, 16, 4096, 136),
+    "small, odd": (101, 2, 3, 16, 73, 131),
+    "small, narrow": (101, 2, 3, 16, 5, 7),
+    "small, odd, ranges": (101, 2, 3, 16, 2051, 61),
+    "128 x 128": (701, 2, 2, 16, 65, 4100),
+    "full": (701, 2, 3, 16, 1032, 4104),
+    "full, ranges": (1030, 1, 1, 16, 7304, 1096),
+}
+
+
+def rows_case(moe, name, seed):
+    """(src [T], w for fwd, offsets, sorted ids, T, topk, reduction, width)"""
+    T, topk, E, bm, red, width = ROWS[name]
+    ids, _, off, _ = moe.moe_align(routing(T, topk, E, seed), E, bm)
+    return bf16((T, red), seed + 1), bf16((E, width, red), seed + 2, red ** -0.5), off, ids
+
+
+# the stream is a forward kernel
+OP_PATHS = [(op, name) for op in ("fwd", "dx") for name in ROWS
+            if op == "fwd" or not name.startswith("stream")]
+
+
+@pytest.mark.parametrize("op,name", OP_PATHS)
+@pytest.mark.parametrize("gather", [True, False], ids=["gather", "sorted"])
+def test_padding_rows_are_zeros_whatever_the_weights_hold(moe, op, name, gather):
+    """Padding rows inside a range are written as zeros, also where the weights
+    hold infinities and NaN (zero times either would be NaN)."""
+    note(f"padding rows, {op} {name} gather={gather}")
+    T, topk, E, bm, red, width = ROWS[name]
+    src, w, off, ids = rows_case(moe, name, 3)
+    w[:, ::3, 0] = float("inf")
+    w[:, 1::3, red // 2] = float("nan")
+    w[:, 2::3, red - 1] = float("-inf")
+    pad = (ids < 0) | (ids >= T * topk)
+    last = int(off[-1])
+    pad[last:] = False                        # in no range: left as they were
+    assert int(pad.sum()) > 0
+    if not gather:
+        src = bf16((ids.shape[0], red), 4)
+        src[(ids < 0) | (ids >= T * topk)] = float("nan")     # not read
+    call = moe.moe_grouped_gemm
+    if op == "dx":
+        w = w.transpose(1, 2).contiguous()
+        call = moe.moe_grouped_gemm_dx
+    out = torch.full((ids.shape[0], width), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = call(src, w, off, sorted_ids=ids, topk=topk, num_tokens=T, gather=gather, out=out)
+    assert (got[pad] == 0).all()
+    assert (got[last:] == 7).all()
+    real = ~pad
+    real[last:] = False
+    assert not torch.isfinite(got[real]).any()
