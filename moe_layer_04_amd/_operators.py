@@ -30,11 +30,12 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _arg(t, name: str, dtype, shape, device):
-    """A dense tensor of this dtype and shape on this GPU.  One expression for
-    the case that everything fits: these checks run before every call, and the
-    shortest kernels here take a few microseconds."""
+    """A dense tensor of this dtype and shape (None: any) on this GPU.  One
+    expression for the case that everything fits: these checks run before every
+    call, and the shortest kernels here take a few microseconds."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        if (t.dtype is dtype and (shape is None or t.shape == shape) and t.device == device
+                and t.is_contiguous()):
             return t
     except AttributeError:
         pass
@@ -44,7 +45,7 @@ def _arg(t, name: str, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
@@ -105,7 +106,7 @@ def _workspace(device, workspace, nbytes: int, product: bool = False):
         if product and nbytes == _UNUSED:
             return _unused(device)
         return _new(torch.uint8, device, nbytes)
-    _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+    _arg(workspace, "workspace", torch.uint8, None, device)
     if workspace.numel() < nbytes:  # an empty one's null pointer would ask for the size
         raise MoEError(MOE_ERR_WORKSPACE, f"workspace of {workspace.numel()} bytes, {nbytes} needed:")
     return workspace
@@ -136,7 +137,9 @@ def _rows(sorted_ids, expert_offsets, num_tokens, gather_from, any_rows: bool, E
         if any_rows:
             raise ValueError("gather and scatter need sorted_ids")
         return 0
-    _arg(sorted_ids, "sorted_ids", _I32, (sorted_ids.numel(),), device)
+    _arg(sorted_ids, "sorted_ids", _I32, None, device)
+    if sorted_ids.dim() != 1:
+        raise ValueError(f"sorted_ids must have one dimension, got {list(sorted_ids.shape)}")
     if gather_from is not None:
         if num_tokens is not None and num_tokens != gather_from:
             raise ValueError(f"num_tokens is {num_tokens}, the gathered operand has "
@@ -159,10 +162,11 @@ def _product(name, rows_in, w, expert_offsets, sorted_ids, topk, num_tokens, gat
     R = count if sorted_ids is None else sorted_ids.shape[0]
     if not gather and count != R:
         raise ValueError(f"the operand has {count} rows, sorted_ids {R}")
-    out = _out(out, "out", _BF16, (T * topk if scatter else R, K if dx else N), dev)
     rows = (MOE_ROWS_GATHER if gather else 0) | (MOE_ROWS_SCATTER if scatter else 0)
     sizes = (rows, T, topk, R, E, K, N)
-    workspace = _workspace(dev, workspace, _product_workspace(name, *sizes), True)
+    need = _product_workspace(name, *sizes)  # refuses sizes before anything is allocated for them
+    out = _out(out, "out", _BF16, (T * topk if scatter else R, K if dx else N), dev)
+    workspace = _workspace(dev, workspace, need, True)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, name, _p(rows_in), _p(w), _p(expert_offsets), _p(sorted_ids), *sizes, _p(out),
           _p(workspace), ctypes.byref(nbytes))
@@ -227,11 +231,12 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
         raise ValueError(f"the gradient must be bfloat16 or float32, got {out_dtype}")
     if accumulate and (out is None or out_dtype is not _F32):
         raise ValueError("accumulate needs a float32 out")
-    out = _out(out, "out", out_dtype, (E, N, K), dev)
     mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype is _F32 else MOE_OUT_BF16
     rows = (MOE_ROWS_GATHER if gather_x else 0) | (MOE_ROWS_GATHER_DY if gather_dy else 0)
     sizes = (rows, T, topk, R, E, K, N, mode)
-    workspace = _workspace(dev, workspace, _product_workspace("moe_grouped_gemm_dw", *sizes), True)
+    need = _product_workspace("moe_grouped_gemm_dw", *sizes)
+    out = _out(out, "out", out_dtype, (E, N, K), dev)
+    workspace = _workspace(dev, workspace, need, True)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, "moe_grouped_gemm_dw", _p(dy), _p(x), _p(expert_offsets), _p(sorted_ids), *sizes,
           _p(out), _p(workspace), ctypes.byref(nbytes))
@@ -246,7 +251,7 @@ def _gated(g, topk_weights, sorted_ids, num_rows):
         raise ValueError("g must have an even number of columns (gate, up)")
     slots = 0
     if topk_weights is not None:
-        _arg(topk_weights, "topk_weights", _F32, topk_weights.shape, dev)
+        _arg(topk_weights, "topk_weights", _F32, None, dev)
         slots = topk_weights.numel()
         if sorted_ids is None and slots != R:
             raise ValueError(f"without sorted_ids topk_weights must have {R} values, got {slots}")

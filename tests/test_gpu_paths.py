@@ -77,3 +77,27 @@ def test_padding_rows_are_zeros_whatever_the_weights_hold(moe, op, name, gather)
     real = ~pad
     real[last:] = False
     assert not torch.isfinite(got[real]).any()
+
+
+def test_refusals_of_sizes_and_of_what_is_no_tensor(moe):
+    """Errors are the binding's own, and come before anything is allocated."""
+    note("refusals of sizes")
+    x, w = bf16((8, 32), 1), bf16((2, 16, 32), 2)
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    ids = torch.arange(8, dtype=torch.int32, device="cuda")
+    for call in (lambda: moe.moe_grouped_gemm(x, w, off, sorted_ids=[0] * 8, gather=True),
+                 lambda: moe.moe_grouped_gemm(x, w, off, sorted_ids=ids.view(2, 4), gather=True),
+                 lambda: moe.moe_grouped_gemm(x, w, off, workspace=bytearray(4096)),
+                 lambda: moe.moe_silu_mul(x, [1.0] * 8)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: moe.moe_grouped_gemm(x, w, off, sorted_ids=ids, num_tokens=-3,
+                                              scatter=True),
+                 lambda: moe.moe_grouped_gemm_dx(bf16((8, 16), 3), w, off, sorted_ids=ids, topk=-2,
+                                                 num_tokens=4, scatter=True),
+                 # an output of 2^60 bytes and more
+                 lambda: moe.moe_grouped_gemm(x, w, off, sorted_ids=ids, num_tokens=1 << 30,
+                                              topk=1 << 26, scatter=True),
+                 lambda: moe.moe_grouped_gemm_dw(x, x, off[:0])):
+        with pytest.raises(moe.MoEError):
+            call()
