@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import MOE_ERR_WORKSPACE, MoEError, _check, load_library
+from ._binding import MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MoEError, _check, load_library
 
 MOE_ROWS_GATHER = 1
 MOE_ROWS_SCATTER = 2
@@ -55,6 +55,13 @@ def _sizes(t, name: str, dims: int):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
         raise ValueError(f"{name} must be a {dims}-dimensional GPU tensor")
     return t.shape
+
+
+def _fit(name: str, *sizes: int):
+    """ctypes cuts sizes to 32 bits without an error: what does not fit is not
+    supported (the library's own limits are lower)."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise MoEError(MOE_ERR_UNSUPPORTED, name)
 
 
 def _new(dtype, device, rows: int, cols: Optional[int] = None) -> torch.Tensor:
@@ -114,6 +121,7 @@ def _workspace(device, workspace, nbytes: int, product: bool = False):
 
 @functools.lru_cache(maxsize=1024)
 def _product_workspace(name: str, *sizes) -> int:
+    _fit(name, *sizes)
     nbytes = ctypes.c_size_t(0)
     _check(_fn(name)(None, None, None, None, *sizes, None, None, ctypes.byref(nbytes), None),
            f"{name} (size query)")
@@ -122,6 +130,7 @@ def _product_workspace(name: str, *sizes) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _norm_workspace(kind: int, M: int, K: int, topk: int, du_topk: int) -> int:
+    _fit("moe_block_norm_bwd", M, K, topk, du_topk)
     nbytes = ctypes.c_size_t(0)
     _check(_fn("moe_block_norm_bwd")(*[None] * 9, kind, M, K, topk, du_topk, 1.0, *[None] * 6,
                                      ctypes.byref(nbytes), None),
@@ -273,6 +282,7 @@ def moe_silu_mul(g: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *
     sorted_ids, 1 without weights).  Padding rows are zero; rows at and past
     num_rows (moe_align's num_padded) are not written."""
     dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
+    _fit("moe_silu_mul", R, N, slots)
     out = _out(out, "out", _BF16, (R, N), dev)
     _call(dev, "moe_silu_mul", _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows), slots, R, N,
           _p(out))
@@ -287,6 +297,7 @@ def moe_silu_mul_bwd(da: torch.Tensor, g: torch.Tensor,
     topk_weights' shape, or None without weights).  Weights of slots that no
     row names get an uninitialised gradient."""
     dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
+    _fit("moe_silu_mul_bwd", R, N, slots)
     _arg(da, "da", _BF16, (R, N), dev)
     dg = torch.empty_like(g)
     dw = None if topk_weights is None else torch.empty_like(topk_weights)
@@ -319,6 +330,7 @@ def moe_block_norm(h: torch.Tensor, o: Optional[torch.Tensor] = None,
     kind = _stream_type(h, "h")
     dev = h.device
     M, K = _sizes(h, "h", 2)
+    _fit("moe_block_norm", M, K, topk)
     _arg(h, "h", h.dtype, (M, K), dev)
     if w_pre is not None:
         _arg(w_pre, "w_pre", _F32, (K,), dev)
@@ -383,12 +395,13 @@ def moe_block_norm_bwd(dh_out: Optional[torch.Tensor], du: Optional[torch.Tensor
         if w_post is not None:
             _arg(w_post, "w_post", _F32, (K,), dev)
             _arg(rstd_post, "rstd_post", _F32, (M,), dev)
+    need = _norm_workspace(kind, M, K, topk, du_topk)
     dh = _new(h_out.dtype, dev, M, K)
     do = None if o is None else _new(_BF16, dev, M, K)
     dgate = None if gate is None else _new(_F32, dev, M)
     dw_post = None if w_post is None else _new(_F32, dev, K)
     dw_pre = None if w_pre is None else _new(_F32, dev, K)
-    workspace = _workspace(dev, workspace, _norm_workspace(kind, M, K, topk, du_topk))
+    workspace = _workspace(dev, workspace, need)
     nbytes = ctypes.c_size_t(workspace.numel())
     _call(dev, "moe_block_norm_bwd", _p(dh_out), _p(du), _p(h_out), _p(o), _p(gate), _p(w_post),
           _p(w_pre), _p(rstd_post), _p(rstd_pre), kind, M, K, topk, du_topk, res_scale, _p(dh),

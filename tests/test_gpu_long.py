@@ -94,3 +94,20 @@ def test_block_norm(moe, K):
     s = moe.moe_block_norm_bwd(few(h), su, sho, few(o), few(gate), wp, wn, sr1, sr2)
     for a, b in ((dh, s[0]), (do, s[1]), (dg, s[2])):
         assert torch.equal(a[at], b)
+
+
+def test_rows_past_32_bits_are_refused(moe):
+    """2^32 + 8 rows are not taken for 8."""
+    note("rows past 32 bits")
+    g = torch.empty(((1 << 32) + 8, 2), dtype=torch.bfloat16, device="cuda")
+    a = g.view(-1)[:g.shape[0]].view(-1, 1)
+    w = torch.ones((1,), device="cuda")
+    x, off = torch.ones((1, 1, 2), dtype=torch.bfloat16, device="cuda"), torch.zeros(
+        2, dtype=torch.int32, device="cuda")
+    for call in (lambda: moe.moe_silu_mul(g), lambda: moe.moe_silu_mul_bwd(a, g),
+                 lambda: moe.moe_block_norm(a, w_pre=w), lambda: moe.moe_grouped_gemm(g, x, off),
+                 lambda: moe.moe_grouped_gemm_dw(a, g, off),
+                 lambda: moe.moe_block_norm_bwd(None, a, a, w_pre=w, rstd_pre=torch.empty(
+                     g.shape[0], device="cuda"))):
+        with pytest.raises(moe.MoEError):
+            call()

@@ -177,3 +177,19 @@ def test_python_refuses_host_tensors():
                                                 rstd_pre=torch.ones(4))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """They are not cut to the 32 bits of the library's arguments: 2^32 + 8
+    rows are not 8."""
+    from moe_layer_04_amd import _operators as O
+    far = (1 << 32) + 8
+    for call in (lambda: O._product_workspace("moe_grouped_gemm", 0, 0, 1, far, 2, 64, 64),
+                 lambda: O._product_workspace("moe_grouped_gemm_dx", 0, far, 1, 16, 2, 64, 64),
+                 lambda: O._product_workspace("moe_grouped_gemm_dw", 0, 0, 1, 16, 2, far, 64, 0),
+                 lambda: O._product_workspace("moe_grouped_gemm", 0, 8, 1 - far, 16, 2, 64, 64),
+                 lambda: O._norm_workspace(0, far, 64, 1, 1),
+                 lambda: O._norm_workspace(0, 4, 64, far, 1)):
+        with pytest.raises(moe.MoEError) as err:
+            call()
+        assert err.value.status == UNS
