@@ -58,11 +58,11 @@ typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
 // What a kernel knows of the widths: multiples of 8, at least 8, or nothing.
 enum class Widths { kWhole, kLong, kAny };
 
-// What chunks outside an operand are loaded from: a branch a chunk costs more (us,
-// with branches / so: 406 rows over 7 experts of 1001 x 330, dx 14.7/11.5; 4096
-// rows over 8 of 4097 x 2049, dw 177/164; but 16 rows over 8 of 14337 x 4095,
-// forward 176/186)
-__device__ const uint16_t kZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+// What chunks outside an operand are loaded from, as one vector of 16 bytes: a
+// branch a chunk costs more (us, with branches / so: 406 rows over 7 experts of
+// 1001 x 330, dx 14.7/11.5; 4096 rows over 8 of 4097 x 2049, dw 177/164; but 16
+// rows over 8 of 14337 x 4095, forward 176/186)
+alignas(16) __device__ const uint16_t kZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
 // Columns c..c+7 of a row of `width`, zeros past its end and for no row.  A
 // row's last chunk is loaded as the row's last 8 values, so that nothing past
