@@ -284,9 +284,9 @@ MOE_API moe_status moe_block_norm_bwd(const void* dh_out, const void* du, const 
     if (!workspace_bytes) return MOE_ERR_INVALID_ARG;
     moe_status st = norm_sizes(h_dtype, M, K, topk, du_topk);
     if (st != MOE_OK) return st;
-    // both weights' partial rows, whichever are asked for: the query has no pointers
+    // for both weights, whichever are asked for: the query has no pointers
     if (workspace_step(workspace, workspace_bytes,
-                       round_up(moe::block_norm_bwd_workspace(M, K, true, true)), &st))
+                       round_up(moe::block_norm_bwd_workspace(M, K)), &st))
         return st;
     if (!w_post != !dw_post || !w_pre != !dw_pre) return MOE_ERR_INVALID_ARG;
     // without rows only the weights' gradients are written, and tensors of the

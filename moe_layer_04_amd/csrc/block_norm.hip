@@ -381,9 +381,8 @@ void launch_block_norm(const NormArgs& a, hipStream_t s) {
     });
 }
 
-size_t block_norm_bwd_workspace(int M, int K, bool post, bool pre) {
-    return (size_t)norm_parts(M, K) * K * 4 * ((post ? 1 : 0) + (pre ? 1 : 0));
-}
+// partial rows of both weights' gradients
+size_t block_norm_bwd_workspace(int M, int K) { return (size_t)norm_parts(M, K) * K * 4 * 2; }
 
 void launch_block_norm_bwd(const NormArgs& a, float* partials, hipStream_t s) {
     const int parts = norm_parts(a.M, a.K);

@@ -14,6 +14,10 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));      // 32 fp8 codes
 typedef unsigned short u16x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x8_t __attribute__((ext_vector_type(8)));
+// the same at any address of an element
+typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
+typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
 
 constexpr int kWave = 64;
 

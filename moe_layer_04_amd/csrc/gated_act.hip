@@ -34,11 +34,10 @@ __device__ __forceinline__ int gated_slot(const GatedArgs& a, int i) {
 template <bool ANY>
 __global__ __launch_bounds__(256) void silu_mul_kernel(GatedArgs a) {
     const uint32_t per_row = ((uint32_t)a.N + V - 1) / V;
-    const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    // (a 32-bit division while the index fits)
-    const uint32_t i = at >> 32 ? (uint32_t)(at / per_row) : (uint32_t)at / per_row;
+    const uint32_t at = blockIdx.x * 256u + threadIdx.x;  // a launch has at most 2^32 threads
+    const uint32_t i = at / per_row;
     if (i >= (uint32_t)a.R) return;
-    const int col = (int)(at - (uint64_t)i * per_row) * V, n = ANY ? min(V, a.N - col) : V;
+    const int col = (int)(at - i * per_row) * V, n = ANY ? min(V, a.N - col) : V;
     const int p = gated_slot(a, (int)i);
     if (p == -2) return;
     const uint16_t* g = a.g + (size_t)i * 2 * a.N + col;

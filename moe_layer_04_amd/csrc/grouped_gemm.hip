@@ -52,9 +52,6 @@ constexpr int kSim = 64;                       // tile and step
 constexpr int kSimBytes = kSim * kSim * 2;     // one operand's step
 constexpr int kSimAhead = 2;                   // steps loaded ahead
 
-typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
-typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
-
 // What a kernel knows of the widths: multiples of 8, at least 8, or nothing.
 enum class Widths { kWhole, kLong, kAny };
 
@@ -365,7 +362,6 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
         for (int a = 0; a < F; ++a) {
             const int col = a0 + fa0 + 16 * a + 4 * (lane >> 4);
             const f32x4_t v = pad ? f32x4_t{0, 0, 0, 0} : acc[a][b];
-            typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
             if (g.splits > 1) {
                 if (col < a_dim)
                     *reinterpret_cast<f32x4_t*>((float*)g.out + ((size_t)sp * g.R + row0 + j) *
@@ -444,7 +440,6 @@ __global__ __launch_bounds__(256) void rows_join_kernel(const float* __restrict_
 #pragma unroll 4
     for (int s = 1; s < g.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(p + s * next);
     uint16_t* o = (uint16_t*)g.out + (size_t)row * width + col;
-    typedef u16x4_t u16x4_any_t __attribute__((aligned(2)));
     u16x4_t q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = f32_to_bf16_bits(v[j]);

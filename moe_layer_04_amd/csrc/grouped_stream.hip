@@ -33,7 +33,6 @@ namespace moe {
 
 namespace {
 
-constexpr uint32_t kNowhere = 0x80000000u;
 constexpr int kRowsA = 32, kRowsB = 16, kStep = 64, kWaves = 4, kAhead = 2;
 constexpr int kWhole = 512;  // longest reduction that a wave takes whole
 

@@ -33,7 +33,6 @@ namespace moe {
 
 namespace {
 
-constexpr uint32_t kNowhere = 0x80000000u;  // an offset no descriptor covers (all are below 2 GiB)
 constexpr int kTile = 256, kStep = 64;
 constexpr int kSlotBytes = kTile * kStep * 2;         // one operand's step
 constexpr int kASlots = 3, kBSlots = 2;

@@ -222,7 +222,7 @@ struct NormArgs {
     float *dgate, *dw_post, *dw_pre;       // backward
 };
 void launch_block_norm(const NormArgs& a, hipStream_t s);
-size_t block_norm_bwd_workspace(int M, int K, bool post, bool pre);
+size_t block_norm_bwd_workspace(int M, int K);
 void launch_block_norm_bwd(const NormArgs& a, float* partials, hipStream_t s);
 
 }  // namespace moe

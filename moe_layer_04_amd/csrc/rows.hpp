@@ -14,8 +14,6 @@ constexpr int V = 8;  // columns a thread takes at a time
 //
 // ONCE: nothing of the line is used again on this XCD soon, and it need not
 // stay in the L2 (rows of whole vectors only: others share lines).
-typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
-typedef u16x8_t u16x8_any_t __attribute__((aligned(2)));
 typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
 
 template <bool ANY, bool ONCE = false>

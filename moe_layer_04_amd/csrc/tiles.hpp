@@ -11,6 +11,9 @@ typedef __amdgpu_buffer_rsrc_t prsrc_t;
 __device__ __forceinline__ prsrc_t pmake_rsrc(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
+// an offset that no descriptor covers (all are below 2 GiB): reads give zeros,
+// stores are dropped
+constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ f32x16_t mfma32_bf16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
