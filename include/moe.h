@@ -477,6 +477,38 @@ moe_status moe_grouped_gemm_dw(const void *dy, const void *x, const int32_t *exp
                                size_t *workspace_bytes, void *stream);
 
 /*
+ * moe_product_plan / moe_grouped_plan -- the launch plan of a product grouped
+ * by expert (`op`): the kernel, the ranges its reduction (dw: an expert's rows)
+ * is cut into, the workgroups of its launch and the workspace's size.  It
+ * depends only on (op, R, E, K, N); the query makes no HIP call.
+ *
+ * Errors: INVALID_ARG for a NULL plan, an unknown op, R < 0, E, K or N < 1;
+ * UNSUPPORTED as the products.
+ */
+typedef enum {
+    MOE_PRODUCT_FWD = 0,       /* moe_grouped_gemm */
+    MOE_PRODUCT_DX = 1,        /* moe_grouped_gemm_dx */
+    MOE_PRODUCT_DW = 2         /* moe_grouped_gemm_dw */
+} moe_product;
+
+typedef enum {
+    MOE_PRODUCT_STREAM = 0,    /* the weight stream of few rows an expert (forward) */
+    MOE_PRODUCT_TILES_64 = 1,  /* 64 x 64, 128 x 128 and 256 x 256 tiles of the output */
+    MOE_PRODUCT_TILES_128 = 2,
+    MOE_PRODUCT_TILES_256 = 3
+} moe_product_kernel;
+
+typedef struct {
+    int32_t kernel;            /* moe_product_kernel */
+    int32_t splits;            /* more than one: a second launch adds the ranges up */
+    int32_t workgroups;        /* of the product's launch; 0: nothing to do */
+    int32_t reserved;          /* zero */
+    uint64_t workspace_bytes;  /* 256: not used */
+} moe_product_plan;
+
+moe_status moe_grouped_plan(int op, int R, int E, int K, int N, moe_product_plan *plan);
+
+/*
  * moe_silu_mul / _bwd -- the gated activation between the two products with
  * the row's routing weight, and its gradients:
  *

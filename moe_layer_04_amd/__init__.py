@@ -12,8 +12,11 @@ from ._binding import (MOE_BF16, FusedForwardGraph, MOE_ERR_HIP, MOE_ERR_INVALID
                        moe_align, moe_align_ex, moe_fused_forward, moe_fused_forward_noalloc,
                        moe_quant_rows_e4m3, moe_topk,
                        status_string, workspace_size)
-from ._operators import (moe_block_norm, moe_block_norm_bwd, moe_grouped_gemm, moe_grouped_gemm_dw,
-                         moe_grouped_gemm_dx, moe_silu_mul, moe_silu_mul_bwd)
+from ._operators import (MOE_PRODUCT_DW, MOE_PRODUCT_DX, MOE_PRODUCT_FWD, MOE_PRODUCT_STREAM,
+                         MOE_PRODUCT_TILES_64, MOE_PRODUCT_TILES_128, MOE_PRODUCT_TILES_256,
+                         ProductPlan, grouped_plan, moe_block_norm, moe_block_norm_bwd,
+                         moe_grouped_gemm, moe_grouped_gemm_dw, moe_grouped_gemm_dx, moe_silu_mul,
+                         moe_silu_mul_bwd)
 
 __all__ = [
     "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_ROWWISE", "MOE_MXFP4_E2M1", "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED",
@@ -23,5 +26,7 @@ __all__ = [
     "FusedForwardGraph", "Plan", "fused_plan", "fused_routing", "moe_fused_forward_noalloc",
     "NOALLOC_SCRATCH_BYTES",
     "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_silu_mul",
-    "moe_silu_mul_bwd", "moe_block_norm", "moe_block_norm_bwd",
+    "moe_silu_mul_bwd", "moe_block_norm", "moe_block_norm_bwd", "ProductPlan", "grouped_plan",
+    "MOE_PRODUCT_FWD", "MOE_PRODUCT_DX", "MOE_PRODUCT_DW", "MOE_PRODUCT_STREAM",
+    "MOE_PRODUCT_TILES_64", "MOE_PRODUCT_TILES_128", "MOE_PRODUCT_TILES_256",
 ]

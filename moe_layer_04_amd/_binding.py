@@ -38,7 +38,7 @@ EXPORTS = ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3", "moe_
            "moe_fused_forward_ex", "moe_fused_forward_timed", "moe_fused_plan",
            "moe_fused_forward_noalloc", "moe_fused_graph_create", "moe_fused_graph_launch",
            "moe_fused_graph_destroy", "moe_grouped_gemm", "moe_grouped_gemm_dx",
-           "moe_grouped_gemm_dw", "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm",
+           "moe_grouped_gemm_dw", "moe_grouped_plan", "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm",
            "moe_block_norm_bwd", "moe_status_string")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # MOE_NOALLOC_SCRATCH_BYTES
@@ -99,6 +99,7 @@ def load_library(build_if_missing: bool = False):
         lib.moe_grouped_gemm.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, SZP, P]
         lib.moe_grouped_gemm_dx.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, SZP, P]
         lib.moe_grouped_gemm_dw.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, SZP, P]
+        lib.moe_grouped_plan.argtypes = [I, I, I, I, I, P]
         lib.moe_silu_mul.argtypes = [P, P, P, P, I, I, I, P, P]
         lib.moe_silu_mul_bwd.argtypes = [P, P, P, P, P, I, I, I, P, P, P]
         lib.moe_block_norm.argtypes = [P, P, P, P, P, I, I, I, I, F, F, P, P, P, P, P]
@@ -106,6 +107,7 @@ def load_library(build_if_missing: bool = False):
                                            P, P, P, SZP, P]
         for name in ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3",
                      "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
+                     "moe_grouped_plan",
                      "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm", "moe_block_norm_bwd",
                      "moe_fused_forward", "moe_fused_forward_ex", "moe_fused_forward_timed",
                      "moe_fused_plan", "moe_fused_forward_noalloc", "moe_fused_graph_create",

@@ -24,6 +24,15 @@ MOE_OUT_BF16 = 0
 MOE_OUT_FP32 = 1
 MOE_OUT_FP32_ADD = 2
 
+MOE_PRODUCT_FWD = 0
+MOE_PRODUCT_DX = 1
+MOE_PRODUCT_DW = 2
+
+MOE_PRODUCT_STREAM = 0
+MOE_PRODUCT_TILES_64 = 1
+MOE_PRODUCT_TILES_128 = 2
+MOE_PRODUCT_TILES_256 = 3
+
 _UNUSED = 256  # workspace bytes of a product that needs none
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -136,6 +145,22 @@ def _norm_workspace(kind: int, M: int, K: int, topk: int, du_topk: int) -> int:
                                      ctypes.byref(nbytes), None),
            "moe_block_norm_bwd (size query)")
     return nbytes.value
+
+
+class ProductPlan(ctypes.Structure):
+    """moe_product_plan of include/moe.h."""
+    _fields_ = [("kernel", ctypes.c_int32), ("splits", ctypes.c_int32),
+                ("workgroups", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+def grouped_plan(op: int, R: int, E: int, K: int, N: int) -> ProductPlan:
+    """The library's launch plan of a product grouped by expert (MOE_PRODUCT_FWD,
+    _DX or _DW) of R sorted rows; no GPU call is made."""
+    _fit("moe_grouped_plan", op, R, E, K, N)
+    plan = ProductPlan()
+    _check(_fn("moe_grouped_plan")(op, R, E, K, N, ctypes.byref(plan)), "moe_grouped_plan")
+    return plan
 
 
 def _rows(sorted_ids, expert_offsets, num_tokens, gather_from, any_rows: bool, E: int, device):

@@ -165,6 +165,24 @@ MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
     return finish();
 }
 
+MOE_API moe_status moe_grouped_plan(int op, int R, int E, int K, int N, moe_product_plan* plan) {
+    if (!plan || op < MOE_PRODUCT_FWD || op > MOE_PRODUCT_DW) return MOE_ERR_INVALID_ARG;
+    moe::GroupedArgs g;
+    const moe_status st = grouped_setup(&g, nullptr, nullptr, 0, 0, 0, 1, R, E, K, N);
+    if (st != MOE_OK) return st;
+    const moe::GroupedPlan p = moe::grouped_plan(g, op);
+    plan->kernel = p.kernel;
+    plan->splits = p.splits;
+    plan->workgroups = p.workgroups;
+    plan->reserved = 0;
+    size_t bytes = op == MOE_PRODUCT_DW   ? moe::grouped_dw_workspace(g)
+                   : op == MOE_PRODUCT_DX ? moe::grouped_dx_workspace(g)
+                                          : moe::grouped_fwd_workspace(g);
+    bytes = product_size(bytes);
+    plan->workspace_bytes = bytes < kAlign ? kAlign : bytes;
+    return MOE_OK;
+}
+
 // ---- the gated activation ------------------------------------------------------
 
 static moe_status gated_check(moe::GatedArgs* a, const void* g, const float* topk_weights,

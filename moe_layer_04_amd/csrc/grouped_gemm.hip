@@ -10,6 +10,7 @@
 // dimension, on the MFMA row dimension, so that a lane's accumulators are
 // neighbours in memory) and "B" (the other one).  Row lookups (gather by
 // token, scatter by slot) happen in the kernels; sums are fp32.
+#include "../../include/moe.h"
 #include "grouped.hpp"
 #include "tiles.hpp"
 
@@ -390,11 +391,14 @@ int blocks_bound(const GroupedArgs& g, int B) {
 // every row of an operand is whole 16-byte chunks
 bool chunked(const GroupedArgs& g) { return g.K % 8 == 0 && g.N % 8 == 0; }
 
+int small_workgroups(const GroupedArgs& g, int op, int tile) {
+    const int a_tiles = ((op == kOpFwd ? g.N : g.K) + tile - 1) / tile;
+    const int b_tiles = op == kOpDw ? g.E * ((g.N + tile - 1) / tile) : blocks_bound(g, tile) * g.splits;
+    return (a_tiles * b_tiles + 7) / 8 * 8;
+}
 template <int OP, Widths W, int TILE>
 void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
-    const int a_tiles = ((OP == kOpFwd ? g.N : g.K) + TILE - 1) / TILE;
-    const int b_tiles = OP == kOpDw ? g.E * ((g.N + TILE - 1) / TILE) : blocks_bound(g, TILE) * g.splits;
-    grouped_small_kernel<OP, W, TILE><<<(a_tiles * b_tiles + 7) / 8 * 8, 256, 0, s>>>(g);
+    grouped_small_kernel<OP, W, TILE><<<small_workgroups(g, OP, TILE), 256, 0, s>>>(g);
 }
 // Rows that are no whole chunks, with enough of them and enough outputs, on 128
 // x 128 tiles: half the loads an output.  us, 64 / 128, T tokens x k over E
@@ -407,7 +411,7 @@ void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
 //   dw  N x K 2048x2/8 4097x2049 [4488] 345/223, 4096x2/8 1025x1025 [648] 101/79,
 //             513x513 [200] 32.5/39.1, 512x2/8 1025x1025 [648] 23.2/23.8
 bool wide(const GroupedArgs& g, int op) {
-    if (chunked(g)) return false;
+    if (chunked(g) || g.K < 8 || g.N < 8) return false;
     const auto tiles = [](int width) { return (long)((width + 2 * kSim - 1) / (2 * kSim)); };
     if (op == kOpDw) return g.E * tiles(g.N) * tiles(g.K) >= 512;
     const long experts = g.R < g.E ? g.R : g.E, blocks = tiles(g.R);
@@ -543,16 +547,6 @@ void launch_rows(const GroupedArgs& call, void* workspace, hipStream_t s) {
         rows_join_kernel<<<(int)((threads + 255) / 256), 256, 0, s>>>((const float*)workspace, g, width);
     }
 }
-}  // namespace
-
-size_t grouped_fwd_workspace(const GroupedArgs& g) { return rows_workspace(g, false); }
-size_t grouped_dx_workspace(const GroupedArgs& g) { return rows_workspace(g, true); }
-void launch_grouped_fwd(const GroupedArgs& g, void* workspace, hipStream_t s) {
-    launch_rows<false>(g, workspace, s);
-}
-void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
-    launch_rows<true>(g, workspace, s);
-}
 
 // The weight gradient on small or on full tiles, by an estimate of what they
 // take in 1/20 us a CU: 11 a step of a small tile (with its share of a CU's four)
@@ -564,7 +558,7 @@ void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
 //   256/8 4096x4096 [32768, 1] 88.5/57.5    19/38 2056x128 [2508, 1] 10.0/21.4
 //   54/73 64x5696 [6497, 1] 17.9/35.3       488/245 576x192 [6615, 1] 21.2/29.7
 //   4096/1 512x512 [64, 64] 47.2/24.0       7448/12 128x3032 [1152, 10] 30.8/22.3
-static bool small_dw(const GroupedArgs& g) {
+bool small_dw(const GroupedArgs& g) {
     if (!chunked(g) || g.R == 0) return true;
     const long experts = g.R < g.E ? g.R : g.E, steps = (g.R / experts + kSim - 1) / kSim;
     auto tiles = [&](int side) { return (long)((g.K + side - 1) / side) * ((g.N + side - 1) / side) * g.E; };
@@ -573,6 +567,41 @@ static bool small_dw(const GroupedArgs& g) {
     const long rounds = (tiles(256) * splits + 255) / 256, part = (steps + splits - 1) / splits;
     return small * (11 * steps + 3) <= 256 * (rounds * (29 * part + 64) + 100);
 }
+}  // namespace
+
+GroupedPlan grouped_plan(const GroupedArgs& call, int op) {
+    static_assert(kOpFwd == MOE_PRODUCT_FWD && kOpDx == MOE_PRODUCT_DX && kOpDw == MOE_PRODUCT_DW, "");
+    if (op != kOpDw && call.R == 0) return {MOE_PRODUCT_TILES_64, 1, 0};  // nothing is launched
+    GroupedArgs g = call;
+    bool stream = false, small;
+    if (op == kOpDw) {
+        small = small_dw(g);
+        g.splits = small ? 1 : grouped_tiles_dw_splits(g);
+    } else {
+        const RowsPlan p = rows_plan(g, op == kOpDx);
+        stream = p.on == RowsPlan::kStream;
+        small = p.on == RowsPlan::kSmall;
+        g.splits = p.splits;
+    }
+    if (stream) return {MOE_PRODUCT_STREAM, g.splits, grouped_stream_workgroups(g)};
+    if (small) {
+        const int tile = wide(g, op) ? 2 * kSim : kSim;
+        return {tile > kSim ? MOE_PRODUCT_TILES_128 : MOE_PRODUCT_TILES_64, g.splits,
+                small_workgroups(g, op, tile)};
+    }
+    return {MOE_PRODUCT_TILES_256, g.splits,
+            op == kOpDw ? grouped_tiles_dw_workgroups(g) : grouped_tiles_rows_workgroups(g, op == kOpDx)};
+}
+
+size_t grouped_fwd_workspace(const GroupedArgs& g) { return rows_workspace(g, false); }
+size_t grouped_dx_workspace(const GroupedArgs& g) { return rows_workspace(g, true); }
+void launch_grouped_fwd(const GroupedArgs& g, void* workspace, hipStream_t s) {
+    launch_rows<false>(g, workspace, s);
+}
+void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
+    launch_rows<true>(g, workspace, s);
+}
+
 size_t grouped_dw_workspace(const GroupedArgs& g) {
     const int splits = small_dw(g) ? 1 : grouped_tiles_dw_splits(g);
     return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;

@@ -140,15 +140,18 @@ __global__ __launch_bounds__(kWaves * 64) void grouped_stream_kernel(GroupedArgs
 
 }  // namespace
 
-void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s) {
+static bool quarters(const GroupedArgs& g) { return g.splits > 1 || g.K > kWhole; }
+
+int grouped_stream_workgroups(const GroupedArgs& g) {
     const int blocks = g.R / kRowsB + (g.R < g.E ? g.R : g.E);
-    if (g.splits > 1 || g.K > kWhole) {
-        const int a_tiles = (g.N + kRowsA - 1) / kRowsA;
-        grouped_stream_kernel<true><<<a_tiles * blocks * g.splits, kWaves * 64, 0, s>>>(g);
-    } else {
-        const int a_tiles = (g.N + kRowsA * kWaves - 1) / (kRowsA * kWaves);
-        grouped_stream_kernel<false><<<a_tiles * blocks, kWaves * 64, 0, s>>>(g);
-    }
+    const int rows = quarters(g) ? kRowsA : kRowsA * kWaves;
+    return (g.N + rows - 1) / rows * blocks * g.splits;
+}
+
+void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s) {
+    const int grid = grouped_stream_workgroups(g);
+    if (quarters(g)) grouped_stream_kernel<true><<<grid, kWaves * 64, 0, s>>>(g);
+    else grouped_stream_kernel<false><<<grid, kWaves * 64, 0, s>>>(g);
 }
 
 }  // namespace moe

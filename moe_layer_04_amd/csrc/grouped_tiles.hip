@@ -860,11 +860,15 @@ static bool rows_look(const GroupedArgs& g, uint32_t how) {
     return g.sorted && !(how == kRowSorted && g.how_out == kRowSlot);
 }
 
+int grouped_tiles_rows_workgroups(const GroupedArgs& g, bool dx) {
+    const int a_tiles = ((dx ? g.K : g.N) + kTile - 1) / kTile;
+    const long most = (long)a_tiles * (g.R / kTile + (g.R < g.E ? g.R : g.E));
+    return (int)((most * g.splits + 7) / 8 * 8);
+}
+
 template <bool DX>
 static void launch_rows_tiles(const GroupedArgs& g, hipStream_t s) {
-    const int a_tiles = ((DX ? g.K : g.N) + kTile - 1) / kTile;
-    const long most = (long)a_tiles * (g.R / kTile + (g.R < g.E ? g.R : g.E));
-    const int grid = (int)((most * g.splits + 7) / 8 * 8);
+    const int grid = grouped_tiles_rows_workgroups(g, DX);
     auto run = [&](auto look, auto parts) {
         grouped_rows_kernel<DX, decltype(look)::value, decltype(parts)::value><<<grid, 512, 0, s>>>(g);
     };
@@ -914,6 +918,11 @@ int grouped_tiles_dw_splits(const GroupedArgs& g) {
     return splits;
 }
 
+int grouped_tiles_dw_workgroups(const GroupedArgs& g) {
+    const long per_xcd = (dw_tiles(g) + 7) / 8 * g.E * g.splits;
+    return 8 * (int)(per_xcd < kCusPerXcd ? per_xcd : kCusPerXcd);
+}
+
 void launch_grouped_tiles_dw(const GroupedArgs& call, void* workspace, hipStream_t s) {
     GroupedArgs g = call;
     if (g.splits > 1) {
@@ -921,8 +930,7 @@ void launch_grouped_tiles_dw(const GroupedArgs& call, void* workspace, hipStream
         g.out_f32 = 1;
         g.accumulate = 0;
     }
-    const long per_xcd = (dw_tiles(g) + 7) / 8 * g.E * g.splits;
-    const int grid = 8 * (int)(per_xcd < kCusPerXcd ? per_xcd : kCusPerXcd);
+    const int grid = grouped_tiles_dw_workgroups(g);
     auto run = [&](auto look, auto out) {
         grouped_dw_kernel<decltype(look)::value, decltype(out)::value><<<grid, 512, 0, s>>>(g);
     };

@@ -182,9 +182,16 @@ void launch_grouped_fwd(const GroupedArgs& g, void* workspace, hipStream_t s);
 void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s);
 size_t grouped_fwd_workspace(const GroupedArgs& g);
 size_t grouped_dx_workspace(const GroupedArgs& g);
+// What the launches above run: moe_product_plan without the workspace's size.
+// op and kernel: moe_product, moe_product_kernel
+struct GroupedPlan { int kernel, splits, workgroups; };
+GroupedPlan grouped_plan(const GroupedArgs& g, int op);
 // very few rows an expert (K and N multiples of 8)
+int grouped_stream_workgroups(const GroupedArgs& g);
 void launch_grouped_stream_fwd(const GroupedArgs& g, hipStream_t s);
 // full 256 x 256 tiles (K and N multiples of 8)
+int grouped_tiles_rows_workgroups(const GroupedArgs& g, bool dx);
+int grouped_tiles_dw_workgroups(const GroupedArgs& g);
 void launch_grouped_tiles_fwd(const GroupedArgs& g, hipStream_t s);
 void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s);
 int grouped_tiles_dw_splits(const GroupedArgs& g);
