@@ -111,3 +111,39 @@ def test_rows_past_32_bits_are_refused(moe):
                      g.shape[0], device="cuda"))):
         with pytest.raises(moe.MoEError):
             call()
+
+
+@pytest.mark.parametrize("slots", [False, True], ids=["plain", "sorted_ids"])
+@pytest.mark.parametrize("K,N", [(64, 8192), (63, 8191)])
+def test_grouped_dw_exactly(moe, K, N, slots):
+    """Every value of the weight gradients of 300000 rows, on small integers:
+    partial sums are at most 4 * 180000 < 2^24, exact in fp32, so that a step
+    of rows lost or read from elsewhere cannot hide behind rounding.  With
+    sorted_ids every 1000th row is padding."""
+    note(f"grouped dw, long, exact, K={K} N={N} sorted_ids={slots}")
+    R, cut = 300_000, 120_000
+    off = torch.tensor([0, cut, cut, R], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def few(rows, cols):
+        t = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+        for i in range(0, rows, 1 << 14):
+            n = min(1 << 14, rows - i)
+            t[i:i + n] = torch.randint(-2, 3, (n, cols), generator=g, device="cuda")
+        return t
+    x, dy = few(R, K), few(R, N)                            # dy: 4.9 GB
+    ids = None
+    if slots:
+        ids = torch.arange(R, dtype=torch.int32, device="cuda")
+        ids[::1000] = R
+        x[::1000] = float("nan")
+    got = moe.moe_grouped_gemm_dw(dy, x, off, sorted_ids=ids, num_tokens=R, out_dtype=torch.float32)
+    want = torch.zeros((3, N, K), dtype=torch.float64, device="cuda")
+    for e, a, b in ((0, 0, cut), (2, cut, R)):
+        for i in range(a, b, 1 << 13):
+            j = min(b, i + (1 << 13))
+            xs = x[i:j].double()
+            if slots:
+                xs[ids[i:j] == R] = 0
+            want[e] += dy[i:j].double().t().contiguous() @ xs
+    assert torch.equal(got, want.float())
