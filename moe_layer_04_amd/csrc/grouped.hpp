@@ -40,15 +40,13 @@ __device__ __forceinline__ int grouped_offset_scalar(const GroupedArgs& g, int e
     return min(max(((scalar_t)g.offsets)[e], 0), g.R);
 }
 
-// Which of the `count` <= 64 rows of a block from its row `first` on are padding
-// rows that the product writes: bit i for row first + i.  They are zeros
-// whatever the weights hold (a row of zeros times an infinity would be NaN).
-// Scattered outputs drop them.  Called by all 64 lanes of a wave.
-__device__ __forceinline__ uint64_t grouped_padding(const GroupedArgs& g, int row0, int rows, int first,
-                                                    int count) {
+// Which of the 64 rows of a block from its row `first` on are padding rows that
+// the product writes: bit i for row first + i.  They are zeros whatever the
+// weights hold (a row of zeros times an infinity would be NaN).  Scattered
+// outputs drop them.  Called by all 64 lanes of a wave.
+__device__ __forceinline__ uint64_t grouped_padding(const GroupedArgs& g, int row0, int rows, int first) {
     if (!g.sorted || g.how_out == kRowSlot) return 0;
-    const int lane = lane_id(), j = first + lane;
-    return __ballot(lane < count && j < rows && (uint32_t)g.sorted[row0 + min(j, rows - 1)] >= g.slots);
+    return __ballot((uint32_t)g.sorted[row0 + min(first + lane_id(), rows - 1)] >= g.slots);
 }
 
 // Rows products cut into g.splits ranges of the reduction leave an fp32 product

@@ -409,7 +409,7 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     // wave tile: 128 columns x 64 rows, 2 x 2 waves in each half of the rows
     const int arow0 = (gw & 1) * 128, brow0 = (wave >> 2) * 128 + (gw >> 1) * 64;
     const bool used = brow0 < blk.rows;
-    const uint64_t padding = LOOK && used ? grouped_padding(g, blk.row0, blk.rows, brow0, 64) : 0;
+    const uint64_t padding = LOOK ? grouped_padding(g, blk.row0, blk.rows, brow0) : 0;
     int steps = (red + kStep - 1) / kStep;
     if constexpr (PARTS) {
         const GroupedRange range = grouped_range(steps, g.splits, sp);
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
     if (used) core.template run<true>(lds, ca, cb, off, steps, wave, arow0, brow0);
     else core.template run<false>(lds, ca, cb, off, steps, wave, arow0, brow0);
     if (used) {
-        if (LOOK && padding) {
+        if (__builtin_expect(padding != 0, 0)) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 if (padding >> (32 * b + (late_lane() & 31)) & 1) {
