@@ -400,8 +400,10 @@ moe_status moe_fused_forward_noalloc(const void *x, const void *w_router,
  *   h', u' = moe_block_norm(h, o, ...)           sums a token's slots, norm after
  *                                                the block, gate, residual, next norm
  *
- * and the backward pass the same calls' gradients in reverse.  (The pages
- * describe the fused forward only; these entry points are not on them.)
+ * and the backward pass the same calls' gradients in reverse.  moe_topk has no
+ * backward: the routing weights' gradient (moe_silu_mul_bwd) is the caller's to
+ * carry on to the router and the tokens.  (The pages describe the fused forward
+ * only; these entry points are not on them.)
  *
  * Sorted rows.  Row i of the R sorted rows belongs to the expert e whose range
  * expert_offsets[e] <= i < expert_offsets[e+1] holds it (moe_align's output;

@@ -14,16 +14,19 @@
 //   do    = s gate rstd_post (b - z mean(b z)),   dgate = s sum(b z)
 //   dw_post = sum_t s gate dh z,                  dw_pre = sum_t du n
 //
-// Bound by HBM: a workgroup holds a whole row in registers, so each value is
-// read and written once and the two sums of a row wait only for each other.
-// Statistics, sums over slots and gradients of the weights are fp32.  The
-// weights' gradients are summed over a workgroup's rows in registers, written
-// as one partial row a workgroup and added up in a fixed order, so results do
-// not depend on the order in which workgroups run.  4096 x 2 rows of 4096, fp32
-// stream: backward 73 + 4.8 us (369 MB, 5 TB/s; the second launch adds up the
-// partial rows); 8 x 2 rows, bf16: forward 4.4 us, a launch and two barriers.
-// 4096 x 2 rows of 4096, bf16: forward 31.8 us with results that do not stay in
-// the L2, 34.4 otherwise; the backward's are 77.3 us in ordinary stores, 78.0 so.
+// Bound by HBM: a workgroup holds a whole row in registers (up to 16384 columns,
+// the backward up to 8192), so each value is read and written once and the two
+// sums of a row wait only for each other; longer rows are read again after a
+// sum.  Statistics, sums over slots and gradients of the weights are fp32.  The
+// weights' gradients are summed over a workgroup's rows, in registers (for
+// longer rows in the partial row itself, read and written for every row),
+// written as one partial row a workgroup and added up in a fixed order, so
+// results do not depend on the order in which workgroups run.  4096 x 2 rows of
+// 4096, fp32 stream: backward 74 + 4.7 us (369 MB, 5 TB/s; the second launch adds
+// up the partial rows); 8 x 2 rows, bf16: forward 4.4 us, a launch and two
+// barriers, backward 5.4 + 2.6.  4096 x 2 rows of 4096, bf16: forward 31.8 us with
+// results that do not stay in the L2, 34.4 otherwise; the backward's are 77.3 us
+// in ordinary stores, 78.0 so.
 #include "common.hpp"
 #include "launch.hpp"
 #include "rows.hpp"
@@ -329,7 +332,13 @@ __global__ __launch_bounds__(kPartCols * kPartRows) void norm_parts_kernel(
 // The backward holds five rows of values and two of sums: one group a thread
 // (126 registers, four waves a SIMD) took 74 us where two groups with half the
 // threads (194 registers, two waves) took 87 (4096 rows of 4096, two slots,
-// fp32 stream: 385 MB).
+// fp32 stream: 385 MB).  1024 threads are one workgroup a CU, which nothing runs
+// beside at its two barriers a row, and with a bf16 stream or odd widths 2 to 6
+// registers short: 4096 x 2 rows of 5120, 7168 and 8192, bf16 94, 110 and 119 us
+// (the bytes' floor 70, 98 and 112), fp32 107, 135 and 151 (96, 134 and 154).
+// Re-read rows: 1024 x 2 of 16384, bf16 127 us (56), fp32 155 (77).  Widths that
+// are no multiples of 8, three waves a SIMD: 4096 x 2 rows of 4095 190 us (56 and
+// 77).
 template <int TH, int C>
 struct Shape {
     static constexpr int kThreads = TH, kGroups = C;

@@ -468,7 +468,10 @@ __global__ __launch_bounds__(512, 2) void grouped_rows_kernel(GroupedArgs g) {
 // costs is the ends of tiles of 16 steps: storing one adds 3-4 us to its 31
 // (32768 rows, 14336 x 4096: 3.05 ms, 1260 TFLOP/s).  Looked-up rows take 7 %
 // more (1930-1960 us): their scalar work is issued between the MFMAs, and with
-// half as much of it again they took 10 %.
+// half as much of it again they took 10 %.  The looked-up case in one run by its
+// output: bf16 2.00 ms, fp32 2.16 and added to fp32 2.74 (plain rows 2.50), whose
+// stores wait for what was there eight times a tile, with five registers spilled
+// where rows are looked up.
 //
 // Tile order: each XCD takes an eighth of every expert's tiles (experts have
 // different numbers of rows; an expert to an XCD would leave most of them
