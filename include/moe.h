@@ -454,7 +454,7 @@ typedef enum {
  *   workspace       as moe_align_ex; the size depends on (rows, T, topk, R, E,
  *                   K, N) and, for dw, out only; 256: it is not used
  *
- * y, dx and dw must not overlap an operand.
+ * y, dx and dw must not overlap an operand (INVALID_ARG).
  *
  * Results do not depend on scheduling: every sum has a fixed order.  R == 0
  * is a no-op for y and dx; dw is written (or left, FP32_ADD).

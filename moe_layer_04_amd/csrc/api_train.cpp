@@ -21,6 +21,12 @@ constexpr long kMaxGather = 1L << 31;   // bytes of a gathered operand, of one e
 bool misaligned(const void* p) { return p && ((uintptr_t)p & 15u); }
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
+// whether two buffers of these many bytes share any
+bool overlap(const void* p, long np, const void* q, long nq) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
+}
+
 moe_status finish() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // workspace == nullptr: reports the size.  Returns true when the call is done.
@@ -97,6 +103,11 @@ moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* o
     if (misaligned(in) || misaligned(w) || misaligned(offsets) || misaligned(sorted_ids) ||
         misaligned(out))
         return MOE_ERR_INVALID_ARG;
+    // workgroups read all of an operand while others write
+    const long slots = (long)T * topk, out_bytes = (rows & MOE_ROWS_SCATTER ? slots : R) * (dx ? K : N) * 2;
+    if (overlap(out, out_bytes, in, (rows & MOE_ROWS_GATHER ? (long)T : R) * (dx ? N : K) * 2) ||
+        overlap(out, out_bytes, w, (long)E * N * K * 2))
+        return MOE_ERR_INVALID_ARG;
     const uint32_t how = rows & MOE_ROWS_GATHER ? moe::kRowToken : moe::kRowSorted;
     g.w = (const uint16_t*)w;
     (dx ? g.dy : g.x) = (const uint16_t*)in;
@@ -154,6 +165,10 @@ MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
         return MOE_ERR_INVALID_ARG;
     if (misaligned(dy) || misaligned(x) || misaligned(expert_offsets) || misaligned(sorted_ids) ||
         misaligned(dw))
+        return MOE_ERR_INVALID_ARG;
+    const long dw_bytes = (long)E * N * K * (g.out_f32 ? 4 : 2);
+    if (overlap(dw, dw_bytes, dy, (rows & MOE_ROWS_GATHER_DY ? (long)T : R) * N * 2) ||
+        overlap(dw, dw_bytes, x, (rows & MOE_ROWS_GATHER ? (long)T : R) * K * 2))
         return MOE_ERR_INVALID_ARG;
     g.dy = (const uint16_t*)dy;
     g.x = (const uint16_t*)x;

@@ -284,3 +284,17 @@ def test_dw_of_clamped_offsets_and_gaps(moe, name):
                                       out=buf[:want.numel()].view(want.shape))
         assert torch.equal(got, want)
         assert (buf[want.numel():] == 7).all()
+
+
+def test_neighbouring_buffers_are_taken(moe):
+    """Operands and output side by side in one allocation, sharing no byte."""
+    note("neighbouring buffers")
+    R, K = 16, 64
+    x, w = ints((R, K), 1), ints((1, K, K), 2)
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    buf = torch.empty((2 * R + K, K), dtype=torch.bfloat16, device="cuda")
+    buf[R:2 * R], buf[2 * R:] = x, w[0]
+    got = moe.moe_grouped_gemm(buf[R:2 * R], buf[2 * R:].view(1, K, K), off, out=buf[:R])
+    assert torch.equal(got, moe.moe_grouped_gemm(x, w, off))
+    with pytest.raises(moe.MoEError):
+        moe.moe_grouped_gemm(buf[R:2 * R], w, off, out=buf[R - 8:2 * R - 8])

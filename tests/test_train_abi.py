@@ -193,3 +193,30 @@ def test_sizes_past_32_bits_are_refused(lib):
         with pytest.raises(moe.MoEError) as err:
             call()
         assert err.value.status == UNS
+
+
+def test_products_over_their_operands_are_refused(lib):
+    """An output that shares bytes with an operand: the same buffer, its end or
+    its middle."""
+    n = ctypes.c_size_t(1 << 40)
+    R, E, K, N = 16, 4, 64, 64
+    at = {"a": 0x100000, "w": 0x200000, "out": 0x300000, "off": 0x400000}
+    size = {"a": R * K * 2, "w": E * N * K * 2}
+
+    def call(name, **kw):
+        p = {k: ctypes.c_void_p(kw.get(k, v)) for k, v in at.items()}
+        return getattr(lib, name)(p["a"], p["w"], p["off"], None, 0, 0, 1, R, E, K, N, p["out"], FAKE,
+                                  ctypes.byref(n), None)
+
+    for name in ("moe_grouped_gemm", "moe_grouped_gemm_dx"):
+        for k in ("a", "w"):
+            for d in (0, 16, size[k] - 16, 16 - R * N * 2):
+                assert call(name, out=at[k] + d) == INV, (name, k, d)
+    bytes_dw = E * N * K * 4
+    for k in ("dy", "x"):
+        for d in (0, 16, R * K * 2 - 16, 16 - bytes_dw):
+            p = {"dy": 0x100000, "x": 0x200000, "dw": 0x300000}
+            p["dw"] = p[k] + d
+            q = {i: ctypes.c_void_p(v) for i, v in p.items()}
+            assert lib.moe_grouped_gemm_dw(q["dy"], q["x"], ctypes.c_void_p(0x400000), None, 0, 0, 1, R, E,
+                                           K, N, 1, q["dw"], FAKE, ctypes.byref(n), None) == INV
