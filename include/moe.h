@@ -539,6 +539,56 @@ moe_status moe_silu_mul_bwd(const void *da, const void *g, const float *topk_wei
                             int N, void *dg, float *dtopk_weights, void *stream);
 
 /*
+ * Activations kept in 8 bits -- what the backward pass reads again, in 1.03
+ * bytes a value.  Blocks of 32 columns of a row (the last one shorter) share a
+ * byte X: a value is code * 2^(X-133), |code| <= 127, with the least X whose
+ * codes reach the block's largest magnitude (OCP MXINT8: an E8M0 scale, 8-bit
+ * integers with 6 fraction bits).  Codes are rounded to nearest, ties to even:
+ * a value is off by at most 1/127 of its block's largest one, and comes back as
+ * the bf16 number that its code stands for, so rows that were brought back are
+ * kept without a further change.  A block with an infinity or a NaN has X = 255
+ * and comes back as NaNs.
+ *
+ *   moe_ckpt_rows             rows of bf16 [R,W] to codes and scales
+ *   moe_ckpt_restore          and back
+ *   moe_silu_mul_ckpt         moe_silu_mul, which also keeps g: its two halves as
+ *                             rows of N (codes and scales as moe_ckpt_rows of
+ *                             [2R,N])
+ *   moe_silu_mul_bwd_ckpt     moe_silu_mul_bwd of what was kept; `a`: the forward's
+ *                             output again, of what was kept (the down weights'
+ *                             gradient reads it)
+ *   moe_grouped_gemm_dw_ckpt  moe_grouped_gemm_dw with x kept in 8 bits
+ *
+ *   codes      int8 [R,W]; of g [R,2N]; of x [R or T,K]
+ *   scales     uint8 [R,ceil(W/32)]; of g [R,2*ceil(N/32)]
+ *   a          moe_silu_mul_bwd_ckpt: out bf16 [R,N], or NULL
+ *   the rest   as the operators of the same names.  Padding rows are kept as
+ *              zeros; rows at and past num_rows stay as they are.  The workspace of
+ *              moe_grouped_gemm_dw_ckpt depends on the same sizes and is always used.
+ *
+ * Outputs must not overlap an input or one another (INVALID_ARG).
+ *
+ * Errors: as those operators; moe_ckpt_rows and moe_ckpt_restore INVALID_ARG for
+ * null or misaligned pointers, R < 0 or W < 1, UNSUPPORTED for R >= 2^28, W >=
+ * 2^20 or R * 4*ceil(W/32) > 2^32 - 256 (which holds for the others' rows too).
+ */
+moe_status moe_ckpt_rows(const void *x, int R, int W, int8_t *codes, uint8_t *scales, void *stream);
+moe_status moe_ckpt_restore(const int8_t *codes, const uint8_t *scales, int R, int W, void *x,
+                            void *stream);
+moe_status moe_silu_mul_ckpt(const void *g, const float *topk_weights, const int32_t *sorted_ids,
+                             const int32_t *num_rows, int slots, int R, int N, void *a,
+                             int8_t *codes, uint8_t *scales, void *stream);
+moe_status moe_silu_mul_bwd_ckpt(const void *da, const int8_t *codes, const uint8_t *scales,
+                                 const float *topk_weights, const int32_t *sorted_ids,
+                                 const int32_t *num_rows, int slots, int R, int N, void *dg,
+                                 float *dtopk_weights, void *a, void *stream);
+moe_status moe_grouped_gemm_dw_ckpt(const void *dy, const int8_t *codes, const uint8_t *scales,
+                                    const int32_t *expert_offsets, const int32_t *sorted_ids,
+                                    int rows, int T, int topk, int R, int E, int K, int N, int out,
+                                    void *dw, void *workspace, size_t *workspace_bytes,
+                                    void *stream);
+
+/*
  * moe_block_norm / _bwd -- the norms after and before a block with the
  * block's gate and residual scale, rms(v)^2 = mean(v^2) + eps:
  *

@@ -132,7 +132,8 @@ def _workspace(device, workspace, nbytes: int, product: bool = False):
 def _product_workspace(name: str, *sizes) -> int:
     _fit(name, *sizes)
     nbytes = ctypes.c_size_t(0)
-    _check(_fn(name)(None, None, None, None, *sizes, None, None, ctypes.byref(nbytes), None),
+    pointers = [None] * (5 if name.endswith("_ckpt") else 4)
+    _check(_fn(name)(*pointers, *sizes, None, None, ctypes.byref(nbytes), None),
            f"{name} (size query)")
     return nbytes.value
 
@@ -245,11 +246,19 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     moe_grouped_gemm's weights: [E,N,K] in ``out_dtype`` (bf16 or fp32), or
     into ``out``; ``accumulate`` adds to an fp32 ``out``.  gather_dy /
     gather_x: that operand has num_tokens rows, read by the rows' tokens."""
-    ny, N = _sizes(dy, "dy", 2)
     nx, K = _sizes(x, "x", 2)
-    dev = dy.device
+    _arg(x, "x", _BF16, (nx, K), x.device)
+    return _product_dw("moe_grouped_gemm_dw", dy, (x,), expert_offsets, sorted_ids, topk, num_tokens,
+                       gather_dy, gather_x, out_dtype, out, accumulate, workspace)
+
+
+def _product_dw(fn, dy, x, expert_offsets, sorted_ids, topk, num_tokens, gather_dy, gather_x, out_dtype,
+                out, accumulate, workspace):
+    """x: the tensors that hold it, the first of its shape (checked)."""
+    nx, K = x[0].shape
+    ny, N = _sizes(dy, "dy", 2)
+    dev = x[0].device
     _arg(dy, "dy", _BF16, (ny, N), dev)
-    _arg(x, "x", _BF16, (nx, K), dev)
     if gather_dy and gather_x and ny != nx:
         raise ValueError("two gathered operands must have the same number of rows")
     E = _sizes(expert_offsets, "expert_offsets", 1)[0] - 1
@@ -268,21 +277,21 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     mode = MOE_OUT_FP32_ADD if accumulate else MOE_OUT_FP32 if out_dtype is _F32 else MOE_OUT_BF16
     rows = (MOE_ROWS_GATHER if gather_x else 0) | (MOE_ROWS_GATHER_DY if gather_dy else 0)
     sizes = (rows, T, topk, R, E, K, N, mode)
-    need = _product_workspace("moe_grouped_gemm_dw", *sizes)
+    need = _product_workspace(fn, *sizes)
     out = _out(out, "out", out_dtype, (E, N, K), dev)
     workspace = _workspace(dev, workspace, need, True)
     nbytes = ctypes.c_size_t(workspace.numel())
-    _call(dev, "moe_grouped_gemm_dw", _p(dy), _p(x), _p(expert_offsets), _p(sorted_ids), *sizes,
-          _p(out), _p(workspace), ctypes.byref(nbytes))
+    _call(dev, fn, _p(dy), *map(_p, x), _p(expert_offsets), _p(sorted_ids), *sizes, _p(out),
+          _p(workspace), ctypes.byref(nbytes))
     return out
 
 
-def _gated(g, topk_weights, sorted_ids, num_rows):
-    R, two_n = _sizes(g, "g", 2)
+def _gated(g, topk_weights, sorted_ids, num_rows, name="g", dtype=_BF16):
+    R, two_n = _sizes(g, name, 2)
     dev = g.device
-    _arg(g, "g", _BF16, (R, two_n), dev)
+    _arg(g, name, dtype, (R, two_n), dev)
     if two_n % 2:
-        raise ValueError("g must have an even number of columns (gate, up)")
+        raise ValueError(f"{name} must have an even number of columns (gate, up)")
     slots = 0
     if topk_weights is not None:
         _arg(topk_weights, "topk_weights", _F32, None, dev)

@@ -3,6 +3,7 @@
 // around the block, with their gradients.  Arguments are checked before any
 // HIP call, as in api.cpp.
 #include "api_checks.hpp"
+#include "ckpt_sizes.hpp"
 #include "launch.hpp"
 
 using namespace moe;
@@ -105,11 +106,13 @@ MOE_API moe_status moe_grouped_gemm_dx(const void* dy, const void* w,
                         workspace, workspace_bytes, stream);
 }
 
-MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
-                                       const int32_t* expert_offsets, const int32_t* sorted_ids,
-                                       int rows, int T, int topk, int R, int E, int K, int N,
-                                       int out, void* dw, void* workspace,
-                                       size_t* workspace_bytes, void* stream) {
+namespace {
+// dw, with x as bf16 rows or (scales given) as rows kept in 8 bits, which are
+// brought back to bf16 in the workspace, before the product's own
+moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* scales,
+                      const int32_t* expert_offsets, const int32_t* sorted_ids, int rows, int T,
+                      int topk, int R, int E, int K, int N, int out, void* dw, void* workspace,
+                      size_t* workspace_bytes, void* stream) {
     if (!workspace_bytes) return MOE_ERR_INVALID_ARG;
     if (out < MOE_OUT_BF16 || out > MOE_OUT_FP32_ADD) return MOE_ERR_INVALID_ARG;
     moe::GroupedArgs g;
@@ -120,21 +123,26 @@ MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
     if (((rows & MOE_ROWS_GATHER) && (long)T * K * 2 >= kMaxGather) ||
         ((rows & MOE_ROWS_GATHER_DY) && (long)T * N * 2 >= kMaxGather))
         return MOE_ERR_UNSUPPORTED;
+    const long x_rows = rows & MOE_ROWS_GATHER ? (long)T : R;
+    if (kept && x_rows * (ckpt_blocks(K) * 4L) > kMaxThreads - 256) return MOE_ERR_UNSUPPORTED;
     g.out_f32 = out != MOE_OUT_BF16;
     g.accumulate = out == MOE_OUT_FP32_ADD;
-    if (workspace_step(workspace, workspace_bytes, product_size(moe::grouped_dw_workspace(g)), &st))
-        return st;
+    size_t need = product_size(moe::grouped_dw_workspace(g));
+    const size_t restored = kept ? round_up((size_t)x_rows * K * 2) : 0;
+    if (restored) need = restored + (need < kAlign ? kAlign : need);
+    if (workspace_step(workspace, workspace_bytes, need, &st)) return st;
     if (R == 0 && g.accumulate) return MOE_OK;
     if (!expert_offsets || !dw) return MOE_ERR_INVALID_ARG;
     if (R > 0 && ((!dy && !(T == 0 && (rows & MOE_ROWS_GATHER_DY))) ||
-                  (!x && !(T == 0 && (rows & MOE_ROWS_GATHER)))))
+                  ((!x || (kept && !scales)) && !(T == 0 && (rows & MOE_ROWS_GATHER)))))
         return MOE_ERR_INVALID_ARG;
-    if (misaligned(dy) || misaligned(x) || misaligned(expert_offsets) || misaligned(sorted_ids) ||
-        misaligned(dw))
+    if (misaligned(dy) || misaligned(x) || misaligned(scales) || misaligned(expert_offsets) ||
+        misaligned(sorted_ids) || misaligned(dw))
         return MOE_ERR_INVALID_ARG;
     const long dw_bytes = (long)E * N * K * (g.out_f32 ? 4 : 2);
     if (overlap(dw, dw_bytes, dy, (rows & MOE_ROWS_GATHER_DY ? (long)T : R) * N * 2) ||
-        overlap(dw, dw_bytes, x, (rows & MOE_ROWS_GATHER ? (long)T : R) * K * 2))
+        overlap(dw, dw_bytes, x, x_rows * K * (kept ? 1 : 2)) ||
+        (kept && overlap(dw, dw_bytes, scales, x_rows * ckpt_blocks(K))))
         return MOE_ERR_INVALID_ARG;
     g.dy = (const uint16_t*)dy;
     g.x = (const uint16_t*)x;
@@ -142,8 +150,31 @@ MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x,
     g.how_dy = rows & MOE_ROWS_GATHER_DY ? moe::kRowToken : moe::kRowSorted;
     g.out = dw;
     (void)hipGetLastError();
-    moe::launch_grouped_dw(g, workspace, (hipStream_t)stream);
+    if (restored && R > 0) {
+        g.x = (const uint16_t*)workspace;
+        moe::launch_ckpt_restore((const int8_t*)x, scales, (int)x_rows, K, (uint16_t*)workspace,
+                                 (hipStream_t)stream);
+    }
+    moe::launch_grouped_dw(g, (char*)workspace + restored, (hipStream_t)stream);
     return finish();
+}
+}  // namespace
+
+MOE_API moe_status moe_grouped_gemm_dw(const void* dy, const void* x, const int32_t* expert_offsets,
+                                       const int32_t* sorted_ids, int rows, int T, int topk, int R,
+                                       int E, int K, int N, int out, void* dw, void* workspace,
+                                       size_t* workspace_bytes, void* stream) {
+    return grouped_dw(dy, x, false, nullptr, expert_offsets, sorted_ids, rows, T, topk, R, E, K, N, out,
+                      dw, workspace, workspace_bytes, stream);
+}
+
+MOE_API moe_status moe_grouped_gemm_dw_ckpt(const void* dy, const int8_t* codes, const uint8_t* scales,
+                                            const int32_t* expert_offsets, const int32_t* sorted_ids,
+                                            int rows, int T, int topk, int R, int E, int K, int N,
+                                            int out, void* dw, void* workspace,
+                                            size_t* workspace_bytes, void* stream) {
+    return grouped_dw(dy, codes, true, scales, expert_offsets, sorted_ids, rows, T, topk, R, E, K, N,
+                      out, dw, workspace, workspace_bytes, stream);
 }
 
 MOE_API moe_status moe_grouped_plan(int op, int R, int E, int K, int N, moe_product_plan* plan) {

@@ -12,8 +12,7 @@
 // 8192 x 14336: backward 211 us (5.6 TB/s), forward 106 us (6.6 TB/s), by loads and
 // stores that keep nothing in the L2 (219 and 117 us by ordinary ones); 16 x
 // 14336: forward 2.7 us, a launch.
-#include "common.hpp"
-#include "launch.hpp"
+#include "gated.hpp"
 #include "rows.hpp"
 
 #include <type_traits>
@@ -21,14 +20,6 @@
 namespace moe {
 
 namespace {
-
-// slot of row i: -1 padding, -2 a row past *num_rows (not touched)
-__device__ __forceinline__ int gated_slot(const GatedArgs& a, int i) {
-    if (a.num_rows && i >= *a.num_rows) return -2;
-    if (!a.sorted) return i;
-    const uint32_t p = (uint32_t)a.sorted[i];
-    return p < a.slots ? (int)p : -1;
-}
 
 // a thread per 8 columns, rows one after the other
 template <bool ANY>

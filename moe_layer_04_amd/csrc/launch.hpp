@@ -213,6 +213,21 @@ struct GatedArgs {
 void launch_silu_mul(const GatedArgs& a, hipStream_t s);
 void launch_silu_mul_bwd(const GatedArgs& a, hipStream_t s);
 
+// ---- rows kept in 8 bits (ckpt.hip; the format: ckpt.hpp) ------------------------
+void launch_ckpt_rows(const uint16_t* x, int R, int W, int8_t* codes, uint8_t* scales, hipStream_t s);
+void launch_ckpt_restore(const int8_t* codes, const uint8_t* scales, int R, int W, uint16_t* x,
+                         hipStream_t s);
+// the activation with what is kept of g: codes [R,2N], scales [R,2*ceil(N/32)]
+struct GatedCkptArgs : GatedArgs {
+    int8_t* codes_out;        // forward
+    uint8_t* scales_out;
+    const int8_t* codes;      // backward, in place of g
+    const uint8_t* scales;
+    uint16_t* again;          // backward: the forward's output from what was kept, or null
+};
+void launch_silu_mul_ckpt(const GatedCkptArgs& a, hipStream_t s);
+void launch_silu_mul_bwd_ckpt(const GatedCkptArgs& a, hipStream_t s);
+
 // ---- the norms around a block (block_norm.hip) -----------------------------------
 struct NormArgs {
     const void* h;                         // forward: h; backward: h_out
