@@ -400,10 +400,10 @@ moe_status moe_fused_forward_noalloc(const void *x, const void *w_router,
  *   h', u' = moe_block_norm(h, o, ...)           sums a token's slots, norm after
  *                                                the block, gate, residual, next norm
  *
- * and the backward pass the same calls' gradients in reverse.  moe_topk has no
- * backward: the routing weights' gradient (moe_silu_mul_bwd) is the caller's to
- * carry on to the router and the tokens.  (The pages describe the fused forward
- * only; these entry points are not on them.)
+ * and the backward pass the same calls' gradients in reverse; the routing
+ * weights' gradient (moe_silu_mul_bwd) goes on to the router and the tokens in
+ * moe_topk_bwd.  (The pages describe the fused forward only; these entry points
+ * are not on them.)
  *
  * Sorted rows.  Row i of the R sorted rows belongs to the expert e whose range
  * expert_offsets[e] <= i < expert_offsets[e+1] holds it (moe_align's output;
@@ -628,6 +628,77 @@ moe_status moe_block_norm_bwd(const void *dh_out, const void *du, const void *h_
                               int K, int topk, int du_topk, float res_scale, void *dh, void *d_o,
                               float *dgate, float *dw_post, float *dw_pre, void *workspace,
                               size_t *workspace_bytes, void *stream);
+
+/*
+ * moe_balance / _bwd -- the balance loss of a router over its experts, the counts
+ * behind it and its gradient.  Of the n tokens that count, with p_t the softmax of
+ * token t's logits over all experts:
+ *
+ *   f_e = counts[e] / (n * topk),  probs[e] = sum_t p_te / n
+ *   loss = E * sum_e f_e * probs[e]
+ *   dlogits[t,e] = dloss * E / n * p_te * (f_e - sum_i p_ti * f_i)
+ *
+ *   logits      fp32 [M,E] (moe_topk's).  A token whose logits are all -inf has
+ *               p = 0
+ *   topk_ids    int32 [M,topk]; ids outside [0,E) are not counted
+ *   token_mask  uint8 [M], 0: the token does not count, and its logits may be
+ *               anything; or NULL: all count
+ *   loss        out fp32 [1];  probs  out fp32 [E]
+ *   counts      int32 [E]: slots that picked expert e;  tokens  int32 [1]: n.
+ *               Outputs of moe_balance, inputs of moe_balance_bwd: summed over
+ *               several batches (or ranks) in between, they give the gradient of
+ *               the loss over all of them
+ *   dloss       fp32 [1], device
+ *   dlogits     out fp32 [M,E], zeros for tokens that do not count
+ *   workspace   as moe_align_ex; its size depends on (M, E)
+ *
+ * n == 0 gives loss, probs and gradients of zero.  Sums are fp32 in a fixed order.
+ * Outputs must not overlap an input or one another (INVALID_ARG).
+ *
+ * Errors: INVALID_ARG for null or misaligned pointers, M < 0, E < 1, topk < 1 or
+ * topk > E; UNSUPPORTED for E > 256, topk > 16 or M*topk >= 2^28; WORKSPACE.
+ */
+moe_status moe_balance(const float *logits, const int32_t *topk_ids, const uint8_t *token_mask,
+                       int M, int E, int topk, float *loss, int32_t *counts, int32_t *tokens,
+                       float *probs, void *workspace, size_t *workspace_bytes, void *stream);
+moe_status moe_balance_bwd(const float *dloss, const float *logits, const int32_t *counts,
+                           const int32_t *tokens, const uint8_t *token_mask, int M, int E,
+                           int topk, float *dlogits, void *stream);
+
+/*
+ * moe_topk_bwd -- the gradients of moe_topk's tokens, weights and bias from those
+ * of the routing weights and of the logits, joined with what the experts sent
+ * back to the tokens:
+ *
+ *   dl[t,e] = dlogits[t,e] + sum over j with topk_ids[t,j] = e of
+ *             w_tj * (dw_tj - sum_i w_ti * dw_ti),  w, dw = (d)topk_weights
+ *   dx[t]   = sum_j dx_rows[t*rows + j] + sum_e dl[t,e] * w_router[e]
+ *   dw[e]   = sum_t dl[t,e] * x[t],   dbias[e] = sum_t dl[t,e]
+ *
+ *   x, w_router    as moe_topk
+ *   topk_ids, topk_weights, dtopk_weights  [M,topk], or all three NULL; ids
+ *                  outside [0,E) pass nothing on
+ *   dlogits        fp32 [M,E] (moe_balance_bwd's), or NULL; one of the two is
+ *                  needed
+ *   dx_rows, rows  bf16 [M*rows,K], a token's rows one after the other
+ *                  (moe_grouped_gemm_dx with scatter: rows = topk), or NULL and 0
+ *   dx             out bf16 [M,K]
+ *   dw, dbias      out fp32 [E,K] and [E]; dbias may be NULL
+ *   workspace      as moe_align_ex; its size depends on (M, K, E)
+ *
+ * dl is fp32; dw and dbias take all of it, dx its upper 16 bits.  Sums are fp32 in
+ * a fixed order.  M == 0 writes zeros to dw and dbias.  Outputs must not overlap an
+ * input or one another (INVALID_ARG).
+ *
+ * Errors: as moe_balance, plus INVALID_ARG for K < 1 or rows < 0 and combinations
+ * other than those above; UNSUPPORTED for K >= 2^20, rows > 16, M*rows >= 2^28 or
+ * 2^24 output tiles of 64 tokens x 128 columns or more.
+ */
+moe_status moe_topk_bwd(const void *x, const void *w_router, const int32_t *topk_ids,
+                        const float *topk_weights, const float *dtopk_weights,
+                        const float *dlogits, const void *dx_rows, int rows, int M, int K, int E,
+                        int topk, void *dx, float *dw, float *dbias, void *workspace,
+                        size_t *workspace_bytes, void *stream);
 
 /* Static, NUL-terminated name of a status code. */
 const char *moe_status_string(int status);

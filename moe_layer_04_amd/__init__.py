@@ -19,6 +19,7 @@ from ._operators import (MOE_PRODUCT_DW, MOE_PRODUCT_DX, MOE_PRODUCT_FWD, MOE_PR
                          moe_silu_mul_bwd)
 from ._checkpoint import (moe_ckpt_restore, moe_ckpt_rows, moe_grouped_gemm_dw_ckpt,
                           moe_silu_mul_bwd_ckpt, moe_silu_mul_ckpt)
+from ._router_grad import moe_balance, moe_balance_bwd, moe_topk_bwd
 
 __all__ = [
     "MOE_BF16", "MOE_FP8_E4M3", "MOE_FP8_E4M3_ROWWISE", "MOE_MXFP4_E2M1", "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED",
@@ -32,5 +33,5 @@ __all__ = [
     "MOE_PRODUCT_FWD", "MOE_PRODUCT_DX", "MOE_PRODUCT_DW", "MOE_PRODUCT_STREAM",
     "MOE_PRODUCT_TILES_64", "MOE_PRODUCT_TILES_128", "MOE_PRODUCT_TILES_256",
     "moe_ckpt_rows", "moe_ckpt_restore", "moe_silu_mul_ckpt", "moe_silu_mul_bwd_ckpt",
-    "moe_grouped_gemm_dw_ckpt",
+    "moe_grouped_gemm_dw_ckpt", "moe_balance", "moe_balance_bwd", "moe_topk_bwd",
 ]

@@ -40,7 +40,8 @@ EXPORTS = ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3", "moe_
            "moe_fused_graph_destroy", "moe_grouped_gemm", "moe_grouped_gemm_dx",
            "moe_grouped_gemm_dw", "moe_grouped_plan", "moe_silu_mul", "moe_silu_mul_bwd", "moe_block_norm",
            "moe_block_norm_bwd", "moe_ckpt_rows", "moe_ckpt_restore", "moe_silu_mul_ckpt",
-           "moe_silu_mul_bwd_ckpt", "moe_grouped_gemm_dw_ckpt", "moe_status_string")
+           "moe_silu_mul_bwd_ckpt", "moe_grouped_gemm_dw_ckpt", "moe_balance", "moe_balance_bwd",
+           "moe_topk_bwd", "moe_status_string")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -111,7 +112,11 @@ def load_library(build_if_missing: bool = False):
         lib.moe_silu_mul_ckpt.argtypes = [P, P, P, P, I, I, I, P, P, P, P]
         lib.moe_silu_mul_bwd_ckpt.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P]
         lib.moe_grouped_gemm_dw_ckpt.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, SZP, P]
+        lib.moe_balance.argtypes = [P, P, P, I, I, I, P, P, P, P, P, SZP, P]
+        lib.moe_balance_bwd.argtypes = [P, P, P, P, P, I, I, I, P, P]
+        lib.moe_topk_bwd.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, SZP, P]
         for name in ("moe_topk", "moe_align", "moe_align_ex", "moe_quant_rows_e4m3",
+                     "moe_balance", "moe_balance_bwd", "moe_topk_bwd",
                      "moe_ckpt_rows", "moe_ckpt_restore", "moe_silu_mul_ckpt",
                      "moe_silu_mul_bwd_ckpt", "moe_grouped_gemm_dw_ckpt",
                      "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",

@@ -26,6 +26,23 @@ inline bool overlap(const void* p, long np, const void* q, long nq) {
     return a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
 }
 
+struct Bytes {
+    const void* p;
+    long n;
+};
+// whether an output shares bytes with an input or with another output
+template <int OUTS, int INS>
+bool overlaps(const Bytes (&outs)[OUTS], const Bytes (&ins)[INS]) {
+    for (int i = 0; i < OUTS; ++i) {
+        if (!outs[i].p) continue;
+        for (const Bytes& in : ins)
+            if (in.p && overlap(outs[i].p, outs[i].n, in.p, in.n)) return true;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+    }
+    return false;
+}
+
 inline moe_status finish() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // workspace == nullptr: reports the size.  Returns true when the call is done.
@@ -40,6 +57,12 @@ inline bool workspace_step(void* workspace, size_t* bytes, size_t need, moe_stat
     else if (*bytes < need) *st = MOE_ERR_WORKSPACE;
     else return false;
     return true;
+}
+
+// The size reported by a call that may not use its workspace: the minimum exactly
+// if it does not, so that a caller may pass any buffer then.
+inline size_t used_size(size_t need) {
+    return need == 0 ? 0 : need < 2 * kAlign ? 2 * kAlign : round_up(need);
 }
 
 }  // namespace moe

@@ -17,23 +17,6 @@ moe_status rows_sizes(int R, int W) {
     return MOE_OK;
 }
 
-struct Bytes {
-    const void* p;
-    long n;
-};
-// whether an output shares bytes with an input or with another output
-template <int OUTS, int INS>
-bool overlaps(const Bytes (&outs)[OUTS], const Bytes (&ins)[INS]) {
-    for (int i = 0; i < OUTS; ++i) {
-        if (!outs[i].p) continue;
-        for (const Bytes& in : ins)
-            if (in.p && overlap(outs[i].p, outs[i].n, in.p, in.n)) return true;
-        for (int j = 0; j < i; ++j)
-            if (outs[j].p && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
-    }
-    return false;
-}
-
 }  // namespace
 
 MOE_API moe_status moe_ckpt_rows(const void* x, int R, int W, int8_t* codes, uint8_t* scales,

@@ -10,12 +10,6 @@ using namespace moe;
 
 namespace {
 
-// The size a product reports: the minimum exactly if it does not use it, so
-// that a caller may pass any buffer then.
-size_t product_size(size_t need) {
-    return need == 0 ? 0 : need < 2 * kAlign ? 2 * kAlign : round_up(need);
-}
-
 // The checks that the three products share; fills g.  `flags`: the moe_rows
 // bits the product knows.
 moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int32_t* sorted_ids,
@@ -61,7 +55,7 @@ moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* o
     if ((rows & MOE_ROWS_GATHER) && (long)T * (dx ? N : K) * 2 >= kMaxGather)
         return MOE_ERR_UNSUPPORTED;
     const size_t need = dx ? moe::grouped_dx_workspace(g) : moe::grouped_fwd_workspace(g);
-    if (workspace_step(workspace, workspace_bytes, product_size(need), &st)) return st;
+    if (workspace_step(workspace, workspace_bytes, used_size(need), &st)) return st;
     if (R == 0) return MOE_OK;
     // with T == 0 every row is padding, and a gathered / scattered operand has no rows
     if ((!in && !(T == 0 && (rows & MOE_ROWS_GATHER))) || !w || !offsets ||
@@ -127,7 +121,7 @@ moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* s
     if (kept && x_rows * (ckpt_blocks(K) * 4L) > kMaxThreads - 256) return MOE_ERR_UNSUPPORTED;
     g.out_f32 = out != MOE_OUT_BF16;
     g.accumulate = out == MOE_OUT_FP32_ADD;
-    size_t need = product_size(moe::grouped_dw_workspace(g));
+    size_t need = used_size(moe::grouped_dw_workspace(g));
     const size_t restored = kept ? round_up((size_t)x_rows * K * 2) : 0;
     if (restored) need = restored + (need < kAlign ? kAlign : need);
     if (workspace_step(workspace, workspace_bytes, need, &st)) return st;
@@ -190,7 +184,7 @@ MOE_API moe_status moe_grouped_plan(int op, int R, int E, int K, int N, moe_prod
     size_t bytes = op == MOE_PRODUCT_DW   ? moe::grouped_dw_workspace(g)
                    : op == MOE_PRODUCT_DX ? moe::grouped_dx_workspace(g)
                                           : moe::grouped_fwd_workspace(g);
-    bytes = product_size(bytes);
+    bytes = used_size(bytes);
     plan->workspace_bytes = bytes < kAlign ? kAlign : bytes;
     return MOE_OK;
 }

@@ -213,6 +213,35 @@ struct GatedArgs {
 void launch_silu_mul(const GatedArgs& a, hipStream_t s);
 void launch_silu_mul_bwd(const GatedArgs& a, hipStream_t s);
 
+// ---- the router's balance loss (balance.hip) and its gradient (router_bwd.hip) -------
+struct BalanceArgs {
+    const float* logits;        // [M,E]
+    const int32_t* ids;         // [M,topk]; forward
+    const uint8_t* mask;        // [M], 0: the token does not count; or null
+    int M, E, topk;
+    float* loss;                // forward: [1], and probs [E]
+    float* probs;
+    int32_t *counts, *tokens;   // forward: out [E], [1]; backward: in
+    const float* dloss;         // backward: [1]
+    float* dlogits;             // backward: [M,E]
+};
+size_t balance_workspace(int M, int E);
+void launch_balance(const BalanceArgs& a, void* workspace, hipStream_t s);
+void launch_balance_bwd(const BalanceArgs& a, hipStream_t s);
+struct RouterBwdArgs {
+    const uint16_t *x, *w;      // [M,K], [E,K]
+    const int32_t* ids;         // [M,topk], or null: no gradient of the weights
+    const float *weights, *dweights;
+    const float* dlogits;       // [M,E], or null
+    const uint16_t* dx_rows;    // [M*rows,K]
+    int rows, M, K, E, topk;
+    uint16_t* dx;               // [M,K]
+    float *dw, *dbias;          // [E,K], [E] or null
+};
+long router_bwd_workgroups(int M, int K, int E);  // of the largest launch
+size_t router_bwd_workspace(int M, int K, int E);
+void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s);
+
 // ---- rows kept in 8 bits (ckpt.hip; the format: ckpt.hpp) ------------------------
 void launch_ckpt_rows(const uint16_t* x, int R, int W, int8_t* codes, uint8_t* scales, hipStream_t s);
 void launch_ckpt_restore(const int8_t* codes, const uint8_t* scales, int R, int W, uint16_t* x,

@@ -1,0 +1,389 @@
+// router_bwd.hip -- the gradient of the router: from those of the routing weights
+// and of the logits to the tokens, the router's weights and its bias.
+//
+//   dl[t,e]  = dlogits[t,e] + sum_{j: id_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+//   dx[t,k]  = sum_j rows[t,j][k] + sum_e dl[t,e] Wr[e,k]
+//   dWr[e,k] = sum_t dl[t,e] x[t,k],   dbias[e] = sum_t dl[t,e]
+//
+// (the weights are the softmax over the picked logits).  A first launch forms dl
+// and leaves it as a sum of bf16 parts, each the rounding of what the ones before
+// it left: two parts hold 16 bits of it, three all 24, and the products run on the
+// bf16 matrix cores with sums in fp32.  dx, which is rounded to bf16 itself, takes
+// two (off by at most 2^-16 of a term), dWr three, so nothing of dl is lost in it.
+#include "launch.hpp"
+#include "rows.hpp"
+#include "small_tiles.hpp"
+
+#include <type_traits>
+
+namespace moe {
+
+namespace {
+
+constexpr int kParts = 3;       // of dl, for dWr
+constexpr int kPartsDx = 2;
+constexpr int kRouterCols = 2 * kSim;  // columns of k a tile
+
+// experts of a row of a part: whole steps and tiles
+__host__ __device__ inline int router_ep(int E) { return (E + kSim - 1) / kSim * kSim; }
+
+// ---- dl -----------------------------------------------------------------------
+// L lanes a token, four experts each; parts [part][token][Ep], zeros past E.
+template <int L, bool VEC>
+__global__ __launch_bounds__(256) void router_dl_kernel(RouterBwdArgs a, uint16_t* __restrict__ parts) {
+    const int lane = lane_id(), e0 = (lane % L) * 4, Ep = router_ep(a.E);
+    const int t = ((int)blockIdx.x * 4 + (int)threadIdx.x / kWave) * (kWave / L) + lane / L;
+    if (t >= a.M) return;
+    f32x4_t v = {0, 0, 0, 0};
+    if (a.dlogits) {
+        const float* row = a.dlogits + (size_t)t * a.E;
+        if constexpr (VEC) {
+            if (e0 < a.E) v = *reinterpret_cast<const f32x4_t*>(row + e0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e0 + i < a.E) v[i] = row[e0 + i];
+        }
+    }
+    if (a.ids) {
+        const size_t p = (size_t)t * a.topk;
+        float mean = 0.0f;
+        for (int j = 0; j < a.topk; ++j) mean += a.weights[p + j] * a.dweights[p + j];
+        for (int j = 0; j < a.topk; ++j) {
+            const int at = a.ids[p + j] - e0;
+            const float g = a.weights[p + j] * (a.dweights[p + j] - mean);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += at == i && e0 + i < a.E ? g : 0.0f;
+        }
+    }
+    if (e0 >= Ep) return;
+    const size_t next = (size_t)a.M * Ep;
+    uint16_t* o = parts + (size_t)t * Ep + e0;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+        const uint2 b = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        *reinterpret_cast<uint2*>(o + q * next) = b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float r = bf16_bits_to_f32(i % 2 ? b[i / 2] >> 16 : b[i / 2] & 0xffffu);
+            v[i] = __builtin_isinf(r) ? 0.0f : v[i] - r;  // (an infinity leaves nothing)
+        }
+    }
+}
+
+// ---- the products' common parts -------------------------------------------------
+// A 64 x 64 piece a thread at a time: rows r and r + 32, chunk c
+struct Piece { u16x8_t v[2]; };
+
+__device__ __forceinline__ void put_piece(char* to, const Piece& p, bool col) {
+    const int r = (int)threadIdx.x >> 3, c = (int)threadIdx.x & 7;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u16x8_t*>(to + (col ? sim_at<true>(r + 32 * h, c) : sim_at<false>(r + 32 * h, c))) = p.v[h];
+}
+// rows row0.. (`rows` of them are there) and columns col0.. of an operand
+template <Widths W>
+__device__ __forceinline__ Piece get_piece(const uint16_t* base, size_t row0, long rows, int ld, int col0) {
+    const int r = (int)threadIdx.x >> 3, c = (int)threadIdx.x & 7;
+    Piece p;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        p.v[h] = load_chunk<W>(r + 32 * h < rows ? base + (row0 + r + 32 * h) * ld : nullptr, col0 + c * 8, ld);
+    return p;
+}
+template <Widths W>
+__device__ __forceinline__ void settle_piece(Piece& p, int ld, int col0) {
+    if constexpr (W != Widths::kWhole) {
+        if (col0 + kSim > ld) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                p.v[h] = settle_chunk(p.v[h], col0 + ((int)threadIdx.x & 7) * 8, ld);
+        }
+    }
+}
+
+// ---- dx -----------------------------------------------------------------------
+// 64 tokens x 128 columns a workgroup; the waves take 32 x 64.  The sums leave through
+// LDS as rows of the tile, where a thread adds the tokens' rows and stores 8
+// columns at a time.
+template <Widths W>
+__global__ __launch_bounds__(256) void router_dx_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts) {
+    __shared__ __attribute__((aligned(16))) char lds[4 * kSimBytes];
+    static_assert(4 * kSimBytes == kSim * kRouterCols * 4, "the tile in fp32 takes the pieces' place");
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols;
+    const int k0 = (int)blockIdx.x % k_tiles * kRouterCols;
+    const size_t t0 = (size_t)((int)blockIdx.x / k_tiles) * kSim;
+    const int Ep = router_ep(a.E), steps = Ep / kSim;
+    const long rows = (long)a.M - (long)t0;
+    f32x4_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+    Piece w[2], d[kPartsDx];
+    auto load = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = get_piece<W>(a.w, (size_t)s * kSim, a.E - s * kSim, a.K, k0 + i * kSim);
+#pragma unroll
+        for (int q = 0; q < kPartsDx; ++q)
+            d[q] = get_piece<Widths::kWhole>(parts + (size_t)q * a.M * Ep, t0, rows, Ep, s * kSim);
+    };
+    load(0);
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            settle_piece<W>(w[i], a.K, k0 + i * kSim);
+            put_piece(lds + i * kSimBytes, w[i], true);
+        }
+#pragma unroll
+        for (int q = 0; q < kPartsDx; ++q) put_piece(lds + (2 + q) * kSimBytes, d[q], false);
+        __syncthreads();
+        if (s + 1 < steps) load(s + 1);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8_t fa[4], fb[kPartsDx][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[i] = sim_frag<true>(lds + (wave & 1) * kSimBytes, 16 * i, ks, lane);
+#pragma unroll
+            for (int q = 0; q < kPartsDx; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    fb[q][j] = sim_frag<false>(lds + (2 + q) * kSimBytes, (wave >> 1) * 32 + 16 * j, ks, lane);
+#pragma unroll
+            for (int q = 0; q < kPartsDx; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[q][j], acc[i][j], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    // chunks of four columns, permuted by the token
+    auto at = [](int token, int chunk) { return token * (kRouterCols * 4) + ((chunk ^ (token & 15)) << 4); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<f32x4_t*>(lds + at((wave >> 1) * 32 + 16 * j + (lane & 15),
+                                                 (wave & 1) * 16 + 4 * i + (lane >> 4))) = acc[i][j];
+    __syncthreads();
+    constexpr bool ANY = W != Widths::kWhole;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int token = i * 16 + tid / 16, c = tid % 16, col = k0 + c * 8;
+        if (token >= rows || col >= a.K) continue;
+        const int n = ANY ? min(V, a.K - col) : V;
+        float f[V];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + at(token, 2 * c + h));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f[4 * h + u] = v[u];
+        }
+        const size_t t = t0 + token;
+        for (int j = 0; j < a.rows; ++j) {
+            float r[V];
+            ld_bf16<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n, r);
+#pragma unroll
+            for (int u = 0; u < V; ++u) f[u] += r[u];
+        }
+        st_bf16<ANY, true>(a.dx + t * a.K + col, n, f);
+    }
+}
+
+// ---- dWr ----------------------------------------------------------------------
+// 64 experts x 128 columns a workgroup over a range of the tokens.  One range
+// writes the results, more leave [range][E][ld] with the bias' sums behind a row.
+__host__ __device__ inline int router_ld(int K) { return (K + 3) / 4 * 4 + 4; }
+
+template <Widths W>
+__global__ __launch_bounds__(256) void router_dw_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
+                                                        int splits, float* __restrict__ sums) {
+    __shared__ __attribute__((aligned(16))) char lds[(2 + kParts) * kSimBytes];
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols, Ep = router_ep(a.E), e_tiles = Ep / kSim;
+    int b = (int)blockIdx.x;
+    const int e0 = b % e_tiles * kSim;
+    b /= e_tiles;
+    const int k0 = b % k_tiles * kRouterCols, sp = b / k_tiles;
+    const int all = (a.M + kSim - 1) / kSim, per = (all + splits - 1) / splits;
+    const int first = min(sp * per, all), steps = min(per, all - first);
+    f32x4_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+    float bias = 0.0f;  // of expert e0 + tid % 64, a quarter of a step's tokens
+    Piece x[2], d[kParts];
+    auto load = [&](int s) {
+        const size_t t0 = (size_t)(first + s) * kSim;
+        const long rows = (long)a.M - (long)t0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[i] = get_piece<W>(a.x, t0, rows, a.K, k0 + i * kSim);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+            d[q] = get_piece<Widths::kWhole>(parts + (size_t)q * a.M * Ep, t0, rows, Ep, e0);
+    };
+    if (steps > 0) load(0);
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            settle_piece<W>(x[i], a.K, k0 + i * kSim);
+            put_piece(lds + i * kSimBytes, x[i], true);
+        }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) put_piece(lds + (2 + q) * kSimBytes, d[q], true);
+        __syncthreads();
+        if (s + 1 < steps) load(s + 1);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8_t fa[4], fb[kParts][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[i] = sim_frag<true>(lds + (wave & 1) * kSimBytes, 16 * i, ks, lane);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    fb[q][j] = sim_frag<true>(lds + (2 + q) * kSimBytes, (wave >> 1) * 32 + 16 * j, ks, lane);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[q][j], acc[i][j], 0, 0, 0);
+        }
+        if (a.dbias && k0 == 0) {
+            const int e = tid % kSim;
+            for (int r = tid / kSim * 16; r < tid / kSim * 16 + 16; ++r) {
+                const char* p = lds + 2 * kSimBytes + sim_at<true>(r, e >> 3) + (e & 7) * 2;
+                float v = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kParts; ++q)  // exact: the parts of one fp32 number
+                    v += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p + q * kSimBytes));
+                bias += v;
+            }
+        }
+        __syncthreads();
+    }
+    const int ld = splits > 1 ? router_ld(a.K) : a.K;
+    float* out = splits > 1 ? sums + (size_t)sp * a.E * ld : a.dw;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int e = e0 + (wave >> 1) * 32 + 16 * j + (lane & 15);
+        if (e >= a.E) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col = k0 + (wave & 1) * kSim + 16 * i + 4 * (lane >> 4);
+            float* o = out + (size_t)e * ld + col;
+            if (col + 4 <= a.K) {
+                *reinterpret_cast<f32x4_any_t*>(o) = acc[i][j];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 3; ++u)
+                    if (col + u < a.K) o[u] = acc[i][j][u];
+            }
+        }
+    }
+    if (a.dbias && k0 == 0) {
+        float* q = reinterpret_cast<float*>(lds);
+        q[tid] = bias;
+        __syncthreads();
+        if (tid < kSim && e0 + tid < a.E) {
+            const float v = (q[tid] + q[tid + 64]) + (q[tid + 128] + q[tid + 192]);
+            if (splits > 1) out[(size_t)(e0 + tid) * ld + ld - 4] = v;
+            else a.dbias[e0 + tid] = v;
+        }
+    }
+}
+
+// the ranges' sums in order, a thread per four values; the last four of a row: the bias
+__global__ __launch_bounds__(256) void router_join_kernel(RouterBwdArgs a, int splits,
+                                                          const float* __restrict__ sums) {
+    const int ld = router_ld(a.K);
+    const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+    const int e = (int)(at / (uint32_t)(ld / 4)), col = (int)(at % (uint32_t)(ld / 4)) * 4;
+    if (e >= a.E) return;
+    const bool bias = col == ld - 4;
+    if (bias && !a.dbias) return;
+    const float* p = sums + (size_t)e * ld + col;
+    const size_t next = (size_t)a.E * ld;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(p + s * next);
+    if (bias) {
+        a.dbias[e] = v[0];
+        return;
+    }
+    float* o = a.dw + (size_t)e * a.K + col;
+    if (col + 4 <= a.K) {
+        *reinterpret_cast<f32x4_any_t*>(o) = v;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+            if (col + u < a.K) o[u] = v[u];
+    }
+}
+
+// Ranges the tokens are cut into: until two workgroups a CU have one, as long as a
+// range keeps four steps.
+int router_splits(int M, int K, int E) {
+    const long tiles = (long)(router_ep(E) / kSim) * ((K + kRouterCols - 1) / kRouterCols);
+    const int steps = (M + kSim - 1) / kSim;
+    int splits = 1;
+    while (splits < 64 && tiles * splits * 2 <= 512 && steps / (splits * 2) >= 4) splits *= 2;
+    return splits;
+}
+
+size_t parts_bytes(int M, int E) { return ((size_t)kParts * M * router_ep(E) * 2 + 255) / 256 * 256; }
+
+}  // namespace
+
+long router_bwd_workgroups(int M, int K, int E) {
+    const long k_tiles = ((long)K + kRouterCols - 1) / kRouterCols;
+    const long dx = ((long)M + kSim - 1) / kSim * k_tiles;
+    const long dw = k_tiles * (router_ep(E) / kSim) * router_splits(M, K, E);
+    return dx > dw ? dx : dw;
+}
+
+size_t router_bwd_workspace(int M, int K, int E) {
+    const int splits = router_splits(M, K, E);
+    return parts_bytes(M, E) + (splits > 1 ? (size_t)splits * E * router_ld(K) * 4 : 0);
+}
+
+void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {
+    uint16_t* parts = (uint16_t*)workspace;
+    float* sums = (float*)((char*)workspace + parts_bytes(a.M, a.E));
+    const int Ep = router_ep(a.E), splits = router_splits(a.M, a.K, a.E);
+    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols;
+    if (a.M > 0) {
+        auto dl = [&](auto lanes) {
+            constexpr int L = decltype(lanes)::value, tokens = 4 * (kWave / L);
+            const int grid = (a.M + tokens - 1) / tokens;
+            if (a.E % 4 == 0) router_dl_kernel<L, true><<<grid, 256, 0, s>>>(a, parts);
+            else router_dl_kernel<L, false><<<grid, 256, 0, s>>>(a, parts);
+        };
+        if (Ep == 64) dl(std::integral_constant<int, 16>{});
+        else if (Ep == 128) dl(std::integral_constant<int, 32>{});
+        else dl(std::integral_constant<int, 64>{});
+    }
+    auto products = [&](auto width) {
+        constexpr Widths W = decltype(width)::value;
+        if (a.M > 0) router_dx_kernel<W><<<(a.M + kSim - 1) / kSim * k_tiles, 256, 0, s>>>(a, parts);
+        router_dw_kernel<W><<<k_tiles * (Ep / kSim) * splits, 256, 0, s>>>(a, parts, splits, sums);
+    };
+    if (a.K % 8 == 0) products(std::integral_constant<Widths, Widths::kWhole>{});
+    else if (a.K >= 8) products(std::integral_constant<Widths, Widths::kLong>{});
+    else products(std::integral_constant<Widths, Widths::kAny>{});
+    if (splits > 1) {
+        const long threads = (long)a.E * (router_ld(a.K) / 4);
+        router_join_kernel<<<(int)((threads + 255) / 256), 256, 0, s>>>(a, splits, sums);
+    }
+}
+
+}  // namespace moe
