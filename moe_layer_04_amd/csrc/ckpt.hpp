@@ -70,23 +70,7 @@ __device__ __forceinline__ void ckpt_values(u32x2_t w, uint32_t X, float (&f)[V]
     for (int i = 0; i < V; ++i) f[i] = (float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * step;
 }
 
-// n of 8 columns of a row, zeros past them (ANY, ONCE: as in rows.hpp)
-template <bool ANY, bool ONCE = false>
-__device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n) {
-    u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
-    if constexpr (!ANY) {
-        if (n <= 0) return v;
-        if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u16x8_t*>(p));
-        else return *reinterpret_cast<const u16x8_t*>(p);
-    } else if (n >= V) {
-        v = *reinterpret_cast<const u16x8_any_t*>(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V - 1; ++i)
-            if (i < n) v[i] = p[i];
-    }
-    return v;
-}
+// n of 8 columns (ANY, ONCE: as in rows.hpp)
 template <bool ANY, bool ONCE = false>
 __device__ __forceinline__ u32x2_t ld_codes(const int8_t* p, int n) {
     u32x2_t w = {0, 0};

@@ -107,14 +107,14 @@ __device__ __forceinline__ void settle_piece(Piece& p, int ld, int col0) {
 // LDS as rows of the tile, where a thread adds the tokens' rows and stores 8
 // columns at a time.
 template <Widths W>
-__global__ __launch_bounds__(256) void router_dx_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts) {
-    __shared__ __attribute__((aligned(16))) char lds[4 * kSimBytes];
+__device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uint16_t* __restrict__ parts, int tile,
+                                               char* lds) {
     static_assert(4 * kSimBytes == kSim * kRouterCols * 4, "the tile in fp32 takes the pieces' place");
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols;
-    const int k0 = (int)blockIdx.x % k_tiles * kRouterCols;
-    const size_t t0 = (size_t)((int)blockIdx.x / k_tiles) * kSim;
+    const int k0 = tile % k_tiles * kRouterCols;
+    const size_t t0 = (size_t)(tile / k_tiles) * kSim;
     const int Ep = router_ep(a.E), steps = Ep / kSim;
     const long rows = (long)a.M - (long)t0;
     f32x4_t acc[4][2];
@@ -171,27 +171,38 @@ __global__ __launch_bounds__(256) void router_dx_kernel(RouterBwdArgs a, const u
             *reinterpret_cast<f32x4_t*>(lds + at((wave >> 1) * 32 + 16 * j + (lane & 15),
                                                  (wave & 1) * 16 + 4 * i + (lane >> 4))) = acc[i][j];
     __syncthreads();
+    // four groups of 8 columns a thread, 16 tokens apart
     constexpr bool ANY = W != Widths::kWhole;
+    const int c = tid % 16, col = k0 + c * 8, n = ANY ? min(V, a.K - col) : V;
+    if (col >= a.K) return;
+    float f[4][V];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int token = i * 16 + tid / 16, c = tid % 16, col = k0 + c * 8;
-        if (token >= rows || col >= a.K) continue;
-        const int n = ANY ? min(V, a.K - col) : V;
-        float f[V];
+        const int token = i * 16 + tid / 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + at(token, 2 * c + h));
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f[4 * h + u] = v[u];
+            for (int u = 0; u < 4; ++u) f[i][4 * h + u] = v[u];
         }
-        const size_t t = t0 + token;
-        for (int j = 0; j < a.rows; ++j) {
-            float r[V];
-            ld_bf16<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n, r);
+    }
+#pragma unroll 2
+    for (int j = 0; j < a.rows; ++j) {
+        u16x8_t r[4];
 #pragma unroll
-            for (int u = 0; u < V; ++u) f[u] += r[u];
+        for (int i = 0; i < 4; ++i) {  // (tokens past the last: the last one's, not stored)
+            const size_t t = t0 + min((long)(i * 16 + tid / 16), rows - 1);
+            r[i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n);
         }
-        st_bf16<ANY, true>(a.dx + t * a.K + col, n, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < V; ++u) f[i][u] += bf16_bits_to_f32(r[i][u]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int token = i * 16 + tid / 16;
+        if (token < rows) st_bf16<ANY, true>(a.dx + (t0 + token) * a.K + col, n, f[i]);
     }
 }
 
@@ -201,13 +212,12 @@ __global__ __launch_bounds__(256) void router_dx_kernel(RouterBwdArgs a, const u
 __host__ __device__ inline int router_ld(int K) { return (K + 3) / 4 * 4 + 4; }
 
 template <Widths W>
-__global__ __launch_bounds__(256) void router_dw_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
-                                                        int splits, float* __restrict__ sums) {
-    __shared__ __attribute__((aligned(16))) char lds[(2 + kParts) * kSimBytes];
+__device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uint16_t* __restrict__ parts, int splits,
+                                               float* __restrict__ sums, int tile, char* lds) {
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols, Ep = router_ep(a.E), e_tiles = Ep / kSim;
-    int b = (int)blockIdx.x;
+    int b = tile;
     const int e0 = b % e_tiles * kSim;
     b /= e_tiles;
     const int k0 = b % k_tiles * kRouterCols, sp = b / k_tiles;
@@ -302,6 +312,17 @@ __global__ __launch_bounds__(256) void router_dw_kernel(RouterBwdArgs a, const u
     }
 }
 
+// Both products in one launch: dWr's tiles, which are bound by the matrix cores and
+// LDS, first, and dx's, which are bound by HBM, beside and behind them.
+template <Widths W>
+__global__ __launch_bounds__(256) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
+                                                              int splits, float* __restrict__ sums, int dw_tiles) {
+    __shared__ __attribute__((aligned(16))) char lds[(2 + kParts) * kSimBytes];
+    const int b = (int)blockIdx.x;
+    if (b < dw_tiles) router_dw_tile<W>(a, parts, splits, sums, b, lds);
+    else router_dx_tile<W>(a, parts, b - dw_tiles, lds);
+}
+
 // the ranges' sums in order, a thread per four values; the last four of a row: the bias
 __global__ __launch_bounds__(256) void router_join_kernel(RouterBwdArgs a, int splits,
                                                           const float* __restrict__ sums) {
@@ -348,7 +369,7 @@ long router_bwd_workgroups(int M, int K, int E) {
     const long k_tiles = ((long)K + kRouterCols - 1) / kRouterCols;
     const long dx = ((long)M + kSim - 1) / kSim * k_tiles;
     const long dw = k_tiles * (router_ep(E) / kSim) * router_splits(M, K, E);
-    return dx > dw ? dx : dw;
+    return dx + dw;
 }
 
 size_t router_bwd_workspace(int M, int K, int E) {
@@ -374,8 +395,8 @@ void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {
     }
     auto products = [&](auto width) {
         constexpr Widths W = decltype(width)::value;
-        if (a.M > 0) router_dx_kernel<W><<<(a.M + kSim - 1) / kSim * k_tiles, 256, 0, s>>>(a, parts);
-        router_dw_kernel<W><<<k_tiles * (Ep / kSim) * splits, 256, 0, s>>>(a, parts, splits, sums);
+        const int dw_tiles = k_tiles * (Ep / kSim) * splits, dx_tiles = (a.M + kSim - 1) / kSim * k_tiles;
+        router_products_kernel<W><<<dw_tiles + dx_tiles, 256, 0, s>>>(a, parts, splits, sums, dw_tiles);
     };
     if (a.K % 8 == 0) products(std::integral_constant<Widths, Widths::kWhole>{});
     else if (a.K >= 8) products(std::integral_constant<Widths, Widths::kLong>{});

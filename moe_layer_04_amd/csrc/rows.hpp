@@ -77,4 +77,21 @@ __device__ __forceinline__ void st_f32(float* p, int n, const float (&f)[V]) {
     }
 }
 
+// the bits of n of 8 columns of a row, zeros past them
+template <bool ANY, bool ONCE = false>
+__device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n) {
+    u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (!ANY) {
+        if (n <= 0) return v;
+        if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u16x8_t*>(p));
+        else return *reinterpret_cast<const u16x8_t*>(p);
+    } else if (n >= V) {
+        v = *reinterpret_cast<const u16x8_any_t*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) v[i] = p[i];
+    }
+    return v;
+}
 }  // namespace moe
