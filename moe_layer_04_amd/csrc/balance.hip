@@ -5,11 +5,12 @@
 //   f_e = c_e / (n k),   P_e = sum_{t in V} p_te / n,   loss = E sum_e f_e P_e
 //   dl_te = dloss E / n  p_te (f_e - sum_i p_ti f_i),   zero rows outside V
 //
-// L lanes share a token, four experts each (L: the least power of two that
-// holds E), so a wave takes 64 / L tokens, and a token's maximum and sums stay
-// within its lanes.  Both passes are bound by HBM: the logits are read once, as 16
-// bytes a lane.  Sums are fp32 in a fixed order: a lane's tokens one after the
-// other, then the lanes, the waves and the workgroups; counts are integers.
+// L <= 16 lanes share a token, and a lane C <= 4 groups of four experts (C > 1 with
+// 16 lanes only), so a wave takes 64 / L tokens, and what a token's maximum and sums
+// cost is shared by them.  Both passes are meant to be bound by HBM: the logits are
+// read once, as 16 bytes a lane and group.  Sums are fp32 in a fixed order: a
+// lane's tokens one after the other, then the lanes, the waves and the workgroups;
+// counts are integers.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -19,222 +20,330 @@ namespace moe {
 
 namespace {
 
-constexpr int kSplit = 4;  // experts a lane
+constexpr int kSplit = 4;     // experts of a group
+constexpr int kGroups = 256;  // workgroups of the forward at most: one a CU
 
-template <int L, typename F>
-__device__ __forceinline__ float group_reduce(float v, F f) {
-    if constexpr (L > 1) v = f(v, __uint_as_float(xchg_u32<0>(__float_as_uint(v))));
-    if constexpr (L > 2) v = f(v, __uint_as_float(xchg_u32<1>(__float_as_uint(v))));
-    if constexpr (L > 4) v = f(v, __uint_as_float(xchg_u32<2>(__float_as_uint(v))));
-    if constexpr (L > 8) v = f(v, __uint_as_float(xchg_u32<3>(__float_as_uint(v))));
-    if constexpr (L > 16) v = f(v, __uint_as_float(xchg_u32<4>(__float_as_uint(v))));
-    if constexpr (L > 32)
-        v = f(__uint_as_float(readlane_u32(__float_as_uint(v), 0)),
-              __uint_as_float(readlane_u32(__float_as_uint(v), 32)));
-    return v;
-}
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-    return group_reduce<L>(v, [](float a, float b) { return a + b; });
-}
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-    return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
-}
+// experts of a token's lane: groups of four, 4 * L apart
+template <int L, int C, bool VEC>
+struct Token {
+    f32x4_t v[C];
 
-// This lane's four logits; -inf past the last expert
-template <bool VEC>
-__device__ __forceinline__ f32x4_t ld_logits(const float* row, int e, int E) {
-    if constexpr (VEC) {
-        if (e < E) return *reinterpret_cast<const f32x4_t*>(row + e);
+    __device__ static __forceinline__ int expert(int c) { return (c * L + lane_id() % L) * kSplit; }
+
+    // -inf past the last expert
+    __device__ __forceinline__ void load(const float* row, int E) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = expert(c);
+#pragma unroll
+            for (int i = 0; i < kSplit; ++i) v[c][i] = -__builtin_inff();
+            if constexpr (VEC) {
+                if (e < E) v[c] = *reinterpret_cast<const f32x4_t*>(row + e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSplit; ++i)
+                    if (e + i < E) v[c][i] = row[e + i];
+            }
+        }
     }
-    f32x4_t v;
-#pragma unroll
-    for (int i = 0; i < kSplit; ++i) v[i] = !VEC && e + i < E ? row[e + i] : -__builtin_inff();
-    return v;
-}
-
-// Probabilities of a token from its lanes' logits; zeros where all are -inf
-// (a NaN makes all of them NaN).
-template <int L>
-__device__ __forceinline__ f32x4_t probabilities(f32x4_t l) {
-    float m = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
-    m = group_max<L>(m);
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    f32x4_t p;
-#pragma unroll
-    for (int i = 0; i < kSplit; ++i) p[i] = __expf(l[i] - base);
-    const float s = group_sum<L>((p[0] + p[1]) + (p[2] + p[3]));
-    const float r = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-    for (int i = 0; i < kSplit; ++i) p[i] *= r;
-    return p;
-}
-
-// loss, counts, tokens and probs from the sums of all tokens, by threads
-// 0..255 of a workgroup (thread e: expert e)
-__device__ __forceinline__ void balance_finish(const BalanceArgs& a, float psum, int count, int n,
-                                               float (&part)[4]) {
-    const int e = (int)threadIdx.x;
-    float term = 0.0f;
-    if (e < a.E) {
-        const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-        const float P = psum * inv;
-        a.counts[e] = count;
-        a.probs[e] = P;
-        term = (float)count * inv / (float)a.topk * P;
+    template <typename F>
+    __device__ static __forceinline__ float reduce(float x, F f) {
+        if constexpr (L > 1) x = f(x, __uint_as_float(xchg_u32<0>(__float_as_uint(x))));
+        if constexpr (L > 2) x = f(x, __uint_as_float(xchg_u32<1>(__float_as_uint(x))));
+        if constexpr (L > 4) x = f(x, __uint_as_float(xchg_u32<2>(__float_as_uint(x))));
+        if constexpr (L > 8) x = f(x, __uint_as_float(xchg_u32<3>(__float_as_uint(x))));
+        return x;
     }
-    if (e == 0) a.tokens[0] = n;
-    term = wave_sum_f32(term);
-    if (e < 256 && lane_id() == 0) part[e / kWave] = term;
-    __syncthreads();
-    if (e == 0) a.loss[0] = (float)a.E * ((part[0] + part[1]) + (part[2] + part[3]));
+    // the sum over the token's experts of g(group, place)
+    template <typename G>
+    __device__ static __forceinline__ float sum(G g) {
+        float x = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) x += (g(c, 0) + g(c, 1)) + (g(c, 2) + g(c, 3));
+        return reduce(x, [](float a, float b) { return a + b; });
+    }
+    // logits to probabilities; zeros where all are -inf (a NaN makes all of them NaN)
+    __device__ __forceinline__ void softmax() {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int c = 0; c < C; ++c) m = fmaxf(fmaxf(fmaxf(v[c][0], v[c][1]), fmaxf(v[c][2], v[c][3])), m);
+        m = reduce(m, [](float a, float b) { return fmaxf(a, b); });
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < kSplit; ++i) v[c][i] = __expf(v[c][i] - base);
+        const float s = sum([&](int c, int i) { return v[c][i]; });
+        const float r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] *= r;
+    }
+};
+
+// counts and probs of expert e from the sums of all tokens; its share of the loss / E
+__device__ __forceinline__ float balance_expert(const BalanceArgs& a, int e, float psum, int count, int n) {
+    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+    const float P = psum * inv;
+    a.counts[e] = count;
+    a.probs[e] = P;
+    return (float)count * inv / (float)a.topk * P;
 }
 
-// A workgroup takes the tokens [b, b + 1) * per; with more than one of them
-// each leaves its sums in the workspace, [groups][E] of p, then of counts, then
-// [groups] of tokens.
-template <int L, bool VEC>
-__global__ __launch_bounds__(256) void balance_kernel(BalanceArgs a, int per, float* __restrict__ psums,
-                                                      int* __restrict__ csums, int* __restrict__ tsums) {
-    __shared__ float sums[4][256];
+// Sums of many workgroups, in the workspace: [groups][E] of p, [groups][E] of
+// counts, [groups] of tokens, a share of the loss for every 32 experts, and how many
+// of these are written.
+constexpr int kJoinExperts = 32, kJoinSlices = 32;
+struct BalanceSums {
+    float* p;
+    int *counts, *tokens;
+    float* shares;
+    uint32_t* done;
+};
+BalanceSums balance_sums(void* workspace, int groups, int E) {
+    BalanceSums s;
+    s.p = (float*)workspace;
+    s.counts = (int*)(s.p + (size_t)groups * E);
+    s.tokens = s.counts + (size_t)groups * E;
+    s.shares = (float*)(s.tokens + groups);
+    s.done = (uint32_t*)(s.shares + 256 / kJoinExperts);
+    return s;
+}
+size_t balance_sums_bytes(int groups, int E) { return ((size_t)groups * (2 * E + 1) + 256 / kJoinExperts + 1) * 4; }
+
+// A workgroup takes the tokens [b, b + 1) * per; with more than one of them each
+// leaves its sums in the workspace.  A wave loads two rounds of tokens and their
+// masks at a time, and a thread its first slot's id before.
+constexpr int kBalanceThreads = 512, kBalanceWaves = kBalanceThreads / kWave, kRounds = 2;
+
+template <int L, int C, bool VEC>
+__global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a, int per, BalanceSums to) {
+    __shared__ float sums[kBalanceWaves][256];
     __shared__ int hist[256];
-    __shared__ int seen[4];
+    __shared__ int seen[kBalanceWaves];
     __shared__ float part[4];
-    constexpr int TW = kWave / L;  // tokens a wave
+    constexpr int TW = kWave / L, kStep = kBalanceWaves * TW;  // tokens a wave, a round
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid / kWave;
     const int first = (int)blockIdx.x * per, last = min(first + per, a.M);
-    const int e0 = (lane % L) * kSplit;
-    hist[tid] = 0;
+    if (tid < 256) hist[tid] = 0;
     __syncthreads();
-    f32x4_t acc = {0, 0, 0, 0};
-    int tokens = 0;
-    for (int t0 = first + wave * TW; t0 < last; t0 += 4 * TW) {
-        const int t = t0 + lane / L;
-        const bool in = t < last && (!a.mask || a.mask[t]);
-        tokens += in && lane % L == 0;
-        f32x4_t l = {0, 0, 0, 0};
-        if (in) l = ld_logits<VEC>(a.logits + (size_t)t * a.E, e0, a.E);
-        const f32x4_t p = probabilities<L>(l);
-        if (in) acc += p;
+    const uint32_t s0 = (uint32_t)first * (uint32_t)a.topk + (uint32_t)tid, s1 = (uint32_t)last * (uint32_t)a.topk;
+    uint32_t pick = 0, valid = 0;
+    if (s0 < s1) {
+        pick = (uint32_t)a.ids[s0];
+        valid = a.mask ? a.mask[s0 / (uint32_t)a.topk] : 1u;
     }
-    const long s0 = (long)first * a.topk, s1 = (long)last * a.topk;
-    for (long s = s0 + tid; s < s1; s += 256) {
-        const uint32_t e = (uint32_t)a.ids[s];
-        if (e < (uint32_t)a.E && (!a.mask || a.mask[s / a.topk])) atomicAdd(&hist[e], 1);
+    f32x4_t acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = f32x4_t{0, 0, 0, 0};
+    int tokens = 0;
+    for (int t0 = first + wave * TW; t0 < last; t0 += kRounds * kStep) {
+        Token<L, C, VEC> p[kRounds];
+        uint32_t in[kRounds];  // masks as loaded: a comparison would wait for them
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int t = t0 + r * kStep + lane / L;
+            in[r] = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) p[r].v[c] = f32x4_t{0, 0, 0, 0};
+            if (t < last) {
+                in[r] = a.mask ? a.mask[t] : 1u;
+                p[r].load(a.logits + (size_t)t * a.E, a.E);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            p[r].softmax();
+            tokens += in[r] != 0 && lane % L == 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (in[r] != 0) acc[c] += p[r].v[c];
+        }
+    }
+    for (uint32_t s = s0; s < s1;) {
+        if (valid != 0 && pick < (uint32_t)a.E) atomicAdd(&hist[pick], 1);
+        s += kBalanceThreads;
+        if (s < s1) {
+            pick = (uint32_t)a.ids[s];
+            valid = a.mask ? a.mask[s / (uint32_t)a.topk] : 1u;
+        }
     }
     // lanes with the same experts, then the waves
 #pragma unroll
-    for (int i = 0; i < kSplit; ++i) {
-        float v = acc[i];
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int d = L; d < kWave; d *= 2) v += __shfl_xor(v, d);
-        if (lane < L) sums[wave][e0 + i] = v;
-    }
+        for (int i = 0; i < kSplit; ++i) {
+            float v = acc[c][i];
+#pragma unroll
+            for (int d = L; d < kWave; d *= 2) v += __shfl_xor(v, d);
+            if (lane < L) sums[wave][Token<L, C, VEC>::expert(c) + i] = v;
+        }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) tokens += __shfl_xor(tokens, d);
     if (lane == 0) seen[wave] = tokens;
     __syncthreads();
-    const float psum = tid < L * kSplit ? (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]) : 0.0f;
-    const int n = (seen[0] + seen[1]) + (seen[2] + seen[3]);
-    if (gridDim.x == 1) {
-        balance_finish(a, psum, hist[tid], n, part);
+    if (tid >= 256) return;
+    float psum = 0.0f;
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kBalanceWaves; ++w) {
+        if (tid < L * C * kSplit) psum += sums[w][tid];
+        n += seen[w];
+    }
+    if (gridDim.x > 1) {
+        if (tid < a.E) {
+            to.p[(size_t)blockIdx.x * a.E + tid] = psum;
+            to.counts[(size_t)blockIdx.x * a.E + tid] = hist[tid];
+        }
+        if (tid == 0) to.tokens[blockIdx.x] = n;
+        if (tid == 0 && blockIdx.x == 0) *to.done = 0;  // for the next launch
         return;
     }
-    if (tid < a.E) {
-        psums[(size_t)blockIdx.x * a.E + tid] = psum;
-        csums[(size_t)blockIdx.x * a.E + tid] = hist[tid];
+    const float term = wave_sum_f32(tid < a.E ? balance_expert(a, tid, psum, hist[tid], n) : 0.0f);
+    if (lane == 0) part[wave] = term;
+    __syncthreads();
+    if (tid == 0) {
+        a.tokens[0] = n;
+        a.loss[0] = (float)a.E * ((part[0] + part[1]) + (part[2] + part[3]));
     }
-    if (tid == 0) tsums[blockIdx.x] = n;
 }
 
-// the workgroups' sums in order: four threads an expert take a quarter of them each
-__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int groups,
-                                                            const float* __restrict__ psums,
-                                                            const int* __restrict__ csums,
-                                                            const int* __restrict__ tsums) {
-    __shared__ float ps[4][256];
-    __shared__ int cs[4][256], ts[4];
-    __shared__ float part[4];
-    const int tid = (int)threadIdx.x, e = tid % 256, q = tid / 256;
-    const int per = (groups + 3) / 4, from = q * per, to = min(from + per, groups);
+// The workgroups' sums in order, 32 experts a workgroup and 32 threads an
+// expert.  The workgroup that is done last adds up the shares of the loss, in the
+// order of the experts whichever it is.  (One workgroup for all of 256 experts
+// is bound by what a CU can load: 7.0 us of 256 groups' sums.)
+__global__ __launch_bounds__(kJoinExperts* kJoinSlices) void balance_join_kernel(BalanceArgs a, int groups,
+                                                                                 BalanceSums from) {
+    __shared__ float ps[kJoinSlices][kJoinExperts];
+    __shared__ int cs[kJoinSlices][kJoinExperts], ts[4];
+    const int tid = (int)threadIdx.x, i = tid % kJoinExperts, q = tid / kJoinExperts;
+    const int e = (int)blockIdx.x * kJoinExperts + i;
     float p = 0.0f;
-    int c = 0, n = 0;
+    int c = 0;
     if (e < a.E) {
 #pragma unroll 8
-        for (int g = from; g < to; ++g) {
-            p += psums[(size_t)g * a.E + e];
-            c += csums[(size_t)g * a.E + e];
+        for (int g = q; g < groups; g += kJoinSlices) {
+            p += from.p[(size_t)g * a.E + e];
+            c += from.counts[(size_t)g * a.E + e];
         }
     }
-    ps[q][e] = p;
-    cs[q][e] = c;
+    ps[q][i] = p;
+    cs[q][i] = c;
     if (tid < 256) {
-        for (int g = tid; g < groups; g += 256) n += tsums[g];
+        int n = tid < groups ? from.tokens[tid] : 0;
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2) n += __shfl_xor(n, d);
         if (lane_id() == 0) ts[tid / kWave] = n;
     }
     __syncthreads();
-    balance_finish(a, (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]),
-                   (cs[0][e] + cs[1][e]) + (cs[2][e] + cs[3][e]), (ts[0] + ts[1]) + (ts[2] + ts[3]), part);
+    if (tid >= kWave) return;
+    const int n = (ts[0] + ts[1]) + (ts[2] + ts[3]);
+    float term = 0.0f;
+    if (tid < kJoinExperts && e < a.E) {
+        p = ps[0][i];
+        c = cs[0][i];
+#pragma unroll
+        for (int s = 1; s < kJoinSlices; ++s) {
+            p += ps[s][i];
+            c += cs[s][i];
+        }
+        term = balance_expert(a, e, p, c, n);
+    }
+    term = wave_sum_f32(term);
+    if (tid != 0) return;
+    if (blockIdx.x == 0) a.tokens[0] = n;
+    __hip_atomic_store(from.shares + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = __hip_atomic_fetch_add(from.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (before + 1 < gridDim.x) return;
+    float loss = 0.0f;
+    for (int b = 0; b < (int)gridDim.x; ++b)
+        loss += __hip_atomic_load(from.shares + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.loss[0] = (float)a.E * loss;
 }
 
-template <int L, bool VEC>
+// (The logits of a token that does not count may be anything: its gradient is
+// written as zeros whatever was computed.)
+constexpr int kBwdGroups = 1024;  // workgroups at most
+
+template <int L, int C, bool VEC>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceArgs a) {
+    typedef Token<L, C, VEC> token_t;
     constexpr int TW = kWave / L;
-    const int lane = lane_id(), e0 = (lane % L) * kSplit;
-    const int n = a.tokens[0];
-    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    f32x4_t f;
-#pragma unroll
-    for (int i = 0; i < kSplit; ++i)
-        f[i] = e0 + i < a.E ? (float)a.counts[e0 + i] * inv / (float)a.topk : 0.0f;
-    const float up = a.dloss[0] * (float)a.E * inv;
     const long stride = (long)gridDim.x * 4 * TW;
-    for (long t0 = ((long)blockIdx.x * 4 + threadIdx.x / kWave) * TW; t0 < a.M; t0 += stride) {
-        const long t = t0 + lane / L;
-        const bool in = t < a.M, counts = in && (!a.mask || a.mask[t]);
-        f32x4_t l = {0, 0, 0, 0};
-        if (counts) l = ld_logits<VEC>(a.logits + (size_t)t * a.E, e0, a.E);
-        f32x4_t p = probabilities<L>(l);
-        const float dot = group_sum<L>((p[0] * f[0] + p[1] * f[1]) + (p[2] * f[2] + p[3] * f[3]));
+    token_t next;
+    uint32_t mask = 1;
+    auto load = [&](long t) {
+        if (t < a.M) {
+            next.load(a.logits + (size_t)t * a.E, a.E);
+            if (a.mask) mask = a.mask[t];
+        }
+    };
 #pragma unroll
-        for (int i = 0; i < kSplit; ++i) p[i] = counts && n > 0 ? up * p[i] * (f[i] - dot) : 0.0f;
-        if (!in) continue;
-        float* o = a.dlogits + (size_t)t * a.E + e0;
-        if constexpr (VEC) {
-            if (e0 < a.E) *reinterpret_cast<f32x4_t*>(o) = p;
-        } else {
+    for (int c = 0; c < C; ++c) next.v[c] = f32x4_t{0, 0, 0, 0};
+    long t0 = ((long)blockIdx.x * 4 + threadIdx.x / kWave) * TW;
+    load(t0 + lane_id() / L);
+    const int n = a.tokens[0];
+    const float inv = n > 0 ? 1.0f / (float)n : 0.0f, share = inv / (float)a.topk;
+    float f[C][kSplit];
 #pragma unroll
-            for (int i = 0; i < kSplit; ++i)
-                if (e0 + i < a.E) o[i] = p[i];
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i) {
+            const int e = token_t::expert(c) + i;
+            f[c][i] = e < a.E ? (float)a.counts[e] * share : 0.0f;
+        }
+    const float up = a.dloss[0] * (float)a.E * inv;
+    for (; t0 < a.M; t0 += stride) {
+        const long t = t0 + lane_id() / L;
+        const bool in = t < a.M, counts = in && n > 0 && mask != 0;
+        token_t p = next;
+        load(t + stride);
+        p.softmax();
+        const float dot = token_t::sum([&](int c, int i) { return p.v[c][i] * f[c][i]; });
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            f32x4_t d;
+#pragma unroll
+            for (int i = 0; i < kSplit; ++i) d[i] = counts ? up * p.v[c][i] * (f[c][i] - dot) : 0.0f;
+            if (!in) continue;
+            const int e = token_t::expert(c);
+            float* o = a.dlogits + (size_t)t * a.E + e;
+            if constexpr (VEC) {
+                if (e < a.E) __builtin_nontemporal_store(d, reinterpret_cast<f32x4_t*>(o));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSplit; ++i)
+                    if (e + i < a.E) o[i] = d[i];
+            }
         }
     }
 }
 
-// calls f(lanes a token, whether rows are whole vectors)
+// calls f(lanes a token, groups a lane, whether rows are whole vectors)
 template <typename F>
 void by_experts(int E, F f) {
-    auto vec = [&](auto lanes) {
-        if (E % kSplit == 0) f(lanes, std::true_type{});
-        else f(lanes, std::false_type{});
+    auto vec = [&](auto lanes, auto groups) {
+        if (E % kSplit == 0) f(lanes, groups, std::true_type{});
+        else f(lanes, groups, std::false_type{});
     };
-    if (E <= 4) vec(std::integral_constant<int, 1>{});
-    else if (E <= 8) vec(std::integral_constant<int, 2>{});
-    else if (E <= 16) vec(std::integral_constant<int, 4>{});
-    else if (E <= 32) vec(std::integral_constant<int, 8>{});
-    else if (E <= 64) vec(std::integral_constant<int, 16>{});
-    else if (E <= 128) vec(std::integral_constant<int, 32>{});
-    else vec(std::integral_constant<int, 64>{});
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 16> most;
+    if (E <= 4) vec(one, one);
+    else if (E <= 8) vec(std::integral_constant<int, 2>{}, one);
+    else if (E <= 16) vec(std::integral_constant<int, 4>{}, one);
+    else if (E <= 32) vec(std::integral_constant<int, 8>{}, one);
+    else if (E <= 64) vec(most, one);
+    else if (E <= 128) vec(most, std::integral_constant<int, 2>{});
+    else if (E <= 192) vec(most, std::integral_constant<int, 3>{});
+    else vec(most, std::integral_constant<int, 4>{});
 }
 
-// Tokens a workgroup: at least 32 rounds of its waves' loads' worth of values,
-// and no more than 256 workgroups.
+// Tokens a workgroup.  All of them while a second launch would cost more than its
+// share of the work (512 tokens of 8 experts: 12 us a call, 16 in two launches);
+// then a load of every thread or more, and a workgroup a CU at most.
 int balance_per(int M, int E) {
-    int per = (8192 + E - 1) / E;
-    if (per < (M + 255) / 256) per = (M + 255) / 256;
-    return per;
+    if ((long)M * E <= 4 * kBalanceThreads * kSplit) return M;
+    const int per = (kBalanceThreads * kSplit + E - 1) / E, share = (M + kGroups - 1) / kGroups;
+    return per > share ? per : share;
 }
 int balance_groups(int M, int E) { return M == 0 ? 1 : (M + balance_per(M, E) - 1) / balance_per(M, E); }
 
@@ -242,27 +351,27 @@ int balance_groups(int M, int E) { return M == 0 ? 1 : (M + balance_per(M, E) - 
 
 size_t balance_workspace(int M, int E) {
     const int groups = balance_groups(M, E);
-    return groups > 1 ? (size_t)groups * (2 * E + 1) * 4 : 0;
+    return groups > 1 ? balance_sums_bytes(groups, E) : 0;
 }
 
 void launch_balance(const BalanceArgs& a, void* workspace, hipStream_t s) {
     const int groups = balance_groups(a.M, a.E), per = balance_per(a.M, a.E);
-    float* psums = (float*)workspace;
-    int* csums = (int*)workspace + (size_t)groups * a.E;
-    int* tsums = csums + (size_t)groups * a.E;
-    by_experts(a.E, [&](auto lanes, auto vec) {
-        balance_kernel<decltype(lanes)::value, decltype(vec)::value><<<groups, 256, 0, s>>>(a, per, psums, csums,
-                                                                                           tsums);
+    const BalanceSums sums = balance_sums(workspace, groups, a.E);
+    by_experts(a.E, [&](auto lanes, auto of_lane, auto vec) {
+        balance_kernel<decltype(lanes)::value, decltype(of_lane)::value, decltype(vec)::value>
+            <<<groups, kBalanceThreads, 0, s>>>(a, per, sums);
     });
-    if (groups > 1) balance_join_kernel<<<1, 1024, 0, s>>>(a, groups, psums, csums, tsums);
+    if (groups > 1)
+        balance_join_kernel<<<(a.E + kJoinExperts - 1) / kJoinExperts, kJoinExperts * kJoinSlices, 0, s>>>(a, groups,
+                                                                                                          sums);
 }
 
 void launch_balance_bwd(const BalanceArgs& a, hipStream_t s) {
-    by_experts(a.E, [&](auto lanes, auto vec) {
+    by_experts(a.E, [&](auto lanes, auto of_lane, auto vec) {
         const long tokens = 4 * (kWave / decltype(lanes)::value);  // of a workgroup at a time
         const long groups = (a.M + tokens - 1) / tokens;
-        balance_bwd_kernel<decltype(lanes)::value, decltype(vec)::value>
-            <<<(int)(groups < 2048 ? groups : 2048), 256, 0, s>>>(a);
+        balance_bwd_kernel<decltype(lanes)::value, decltype(of_lane)::value, decltype(vec)::value>
+            <<<(int)(groups < kBwdGroups ? groups : kBwdGroups), 256, 0, s>>>(a);
     });
 }
 
