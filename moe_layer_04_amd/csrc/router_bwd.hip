@@ -28,21 +28,26 @@ constexpr int kRouterCols = 2 * kSim;  // columns of k a tile
 __host__ __device__ inline int router_ep(int E) { return (E + kSim - 1) / kSim * kSim; }
 
 // ---- dl -----------------------------------------------------------------------
-// L lanes a token, four experts each; parts [part][token][Ep], zeros past E.
-template <int L, bool VEC>
-__global__ __launch_bounds__(256) void router_dl_kernel(RouterBwdArgs a, uint16_t* __restrict__ parts) {
-    const int lane = lane_id(), e0 = (lane % L) * 4, Ep = router_ep(a.E);
-    const int t = ((int)blockIdx.x * 4 + (int)threadIdx.x / kWave) * (kWave / L) + lane / L;
-    if (t >= a.M) return;
-    f32x4_t v = {0, 0, 0, 0};
+// dl of N experts from e0 on of token t (VEC: rows of dlogits are whole vectors)
+template <int N, bool VEC>
+__device__ __forceinline__ void router_dl(const RouterBwdArgs& a, int t, int e0, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
     if (a.dlogits) {
         const float* row = a.dlogits + (size_t)t * a.E;
-        if constexpr (VEC) {
-            if (e0 < a.E) v = *reinterpret_cast<const f32x4_t*>(row + e0);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e0 + i < a.E) v[i] = row[e0 + i];
+        for (int i = 0; i < N; i += 4) {
+            if constexpr (VEC) {
+                if (e0 + i < a.E) {
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(row + e0 + i);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v[i + u] = x[u];
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (e0 + i + u < a.E) v[i + u] = row[e0 + i + u];
+            }
         }
     }
     if (a.ids) {
@@ -50,29 +55,39 @@ __global__ __launch_bounds__(256) void router_dl_kernel(RouterBwdArgs a, uint16_
         float mean = 0.0f;
         for (int j = 0; j < a.topk; ++j) mean += a.weights[p + j] * a.dweights[p + j];
         for (int j = 0; j < a.topk; ++j) {
-            const int at = a.ids[p + j] - e0;
+            const int e = a.ids[p + j];
             const float g = a.weights[p + j] * (a.dweights[p + j] - mean);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += at == i && e0 + i < a.E ? g : 0.0f;
-        }
-    }
-    if (e0 >= Ep) return;
-    const size_t next = (size_t)a.M * Ep;
-    uint16_t* o = parts + (size_t)t * Ep + e0;
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) {
-        const uint2 b = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        *reinterpret_cast<uint2*>(o + q * next) = b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float r = bf16_bits_to_f32(i % 2 ? b[i / 2] >> 16 : b[i / 2] & 0xffffu);
-            v[i] = __builtin_isinf(r) ? 0.0f : v[i] - r;  // (an infinity leaves nothing)
+            for (int i = 0; i < N; ++i) v[i] += e == e0 + i && e < a.E ? g : 0.0f;
         }
     }
 }
+// The next part of values, which are left with what it does not hold
+__device__ __forceinline__ uint32_t next_part(float& lo, float& hi) {
+    const uint32_t b = pack_bf16x2(lo, hi);
+    const float x = bf16_bits_to_f32(b & 0xffffu), y = bf16_bits_to_f32(b >> 16);
+    lo = __builtin_isinf(x) ? 0.0f : lo - x;  // (an infinity leaves nothing)
+    hi = __builtin_isinf(y) ? 0.0f : hi - y;
+    return b;
+}
+
+// L lanes a token, four experts each; parts [part][token][Ep], zeros past E.
+template <int L, bool VEC>
+__global__ __launch_bounds__(256) void router_dl_kernel(RouterBwdArgs a, uint16_t* __restrict__ parts) {
+    const int lane = lane_id(), e0 = (lane % L) * 4, Ep = router_ep(a.E);
+    const int t = ((int)blockIdx.x * 4 + (int)threadIdx.x / kWave) * (kWave / L) + lane / L;
+    if (t >= a.M || e0 >= Ep) return;
+    float v[4];
+    router_dl<4, VEC>(a, t, e0, v);
+    const size_t next = (size_t)a.M * Ep;
+    uint16_t* o = parts + (size_t)t * Ep + e0;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+        *reinterpret_cast<uint2*>(o + q * next) = uint2{next_part(v[0], v[1]), next_part(v[2], v[3])};
+}
 
 // ---- the products' common parts -------------------------------------------------
-// A 64 x 64 piece a thread at a time: rows r and r + 32, chunk c
+// A 64 x 64 piece of an operand, a thread's share of it: rows r and r + 32, chunk c
 struct Piece { u16x8_t v[2]; };
 
 __device__ __forceinline__ void put_piece(char* to, const Piece& p, bool col) {
@@ -81,15 +96,54 @@ __device__ __forceinline__ void put_piece(char* to, const Piece& p, bool col) {
     for (int h = 0; h < 2; ++h)
         *reinterpret_cast<u16x8_t*>(to + (col ? sim_at<true>(r + 32 * h, c) : sim_at<false>(r + 32 * h, c))) = p.v[h];
 }
-// rows row0.. (`rows` of them are there) and columns col0.. of an operand
+// Rows of `ld` elements from `base` on, `rows` of them, columns col0..; rows of whole
+// chunks through a descriptor that ends with the last row: what lies outside is
+// zeros and costs no instruction.
 template <Widths W>
-__device__ __forceinline__ Piece get_piece(const uint16_t* base, size_t row0, long rows, int ld, int col0) {
+__device__ __forceinline__ Piece get_piece(const uint16_t* base, long rows, int ld, int col0) {
     const int r = (int)threadIdx.x >> 3, c = (int)threadIdx.x & 7;
     Piece p;
+    if constexpr (W == Widths::kWhole) {
+        const prsrc_t src = pmake_rsrc(base, (uint32_t)(min(rows, (long)kSim) * ld * 2));
+        const uint32_t col = (uint32_t)(col0 + c * 8);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        p.v[h] = load_chunk<W>(r + 32 * h < rows ? base + (row0 + r + 32 * h) * ld : nullptr, col0 + c * 8, ld);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = col < (uint32_t)ld ? ((uint32_t)(r + 32 * h) * (uint32_t)ld + col) * 2 : kNowhere;
+            p.v[h] = __builtin_bit_cast(u16x8_t, __builtin_amdgcn_raw_buffer_load_b128(src, at, 0, 0));
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            p.v[h] = load_chunk<W>(r + 32 * h < rows ? base + (size_t)(r + 32 * h) * ld : nullptr, col0 + c * 8, ld);
+    }
     return p;
+}
+// The same of dl's parts, 64 tokens from t0 on and experts e0..: as the launch
+// before left them, or formed here
+template <int PARTS, bool IN_PLACE>
+__device__ __forceinline__ void get_parts(const RouterBwdArgs& a, const uint16_t* parts, size_t t0, int e0,
+                                          Piece (&d)[PARTS]) {
+    const long rows = (long)a.M - (long)t0;
+    if constexpr (!IN_PLACE) {
+        const int Ep = router_ep(a.E);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+            d[q] = get_piece<Widths::kWhole>(parts + ((size_t)q * a.M + t0) * Ep, rows, Ep, e0);
+    } else {
+        const int r = (int)threadIdx.x >> 3, c = (int)threadIdx.x & 7;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8] = {};
+            if (r + 32 * h < rows && e0 + c * 8 < a.E)
+                router_dl<8, false>(a, (int)t0 + r + 32 * h, e0 + c * 8, v);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                const uint4 b = {next_part(v[0], v[1]), next_part(v[2], v[3]), next_part(v[4], v[5]),
+                                 next_part(v[6], v[7])};
+                d[q].v[h] = __builtin_bit_cast(u16x8_t, b);
+            }
+        }
+    }
 }
 template <Widths W>
 __device__ __forceinline__ void settle_piece(Piece& p, int ld, int col0) {
@@ -106,16 +160,15 @@ __device__ __forceinline__ void settle_piece(Piece& p, int ld, int col0) {
 // 64 tokens x 128 columns a workgroup; the waves take 32 x 64.  The sums leave through
 // LDS as rows of the tile, where a thread adds the tokens' rows and stores 8
 // columns at a time.
-template <Widths W>
+template <Widths W, bool IN_PLACE>
 __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uint16_t* __restrict__ parts, int tile,
                                                char* lds) {
-    static_assert(4 * kSimBytes == kSim * kRouterCols * 4, "the tile in fp32 takes the pieces' place");
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols;
     const int k0 = tile % k_tiles * kRouterCols;
     const size_t t0 = (size_t)(tile / k_tiles) * kSim;
-    const int Ep = router_ep(a.E), steps = Ep / kSim;
+    const int steps = (a.E + kSim - 1) / kSim;
     const long rows = (long)a.M - (long)t0;
     f32x4_t acc[4][2];
 #pragma unroll
@@ -126,11 +179,10 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
     auto load = [&](int s) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            w[i] = get_piece<W>(a.w, (size_t)s * kSim, a.E - s * kSim, a.K, k0 + i * kSim);
-#pragma unroll
-        for (int q = 0; q < kPartsDx; ++q)
-            d[q] = get_piece<Widths::kWhole>(parts + (size_t)q * a.M * Ep, t0, rows, Ep, s * kSim);
+            w[i] = get_piece<W>(a.w + (size_t)s * kSim * a.K, a.E - s * kSim, a.K, k0 + i * kSim);
+        get_parts<kPartsDx, IN_PLACE>(a, parts, t0, s * kSim, d);
     };
+    auto part = [&](int q) { return lds + (2 + q) * kSimBytes; };
     load(0);
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
@@ -139,26 +191,26 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
             put_piece(lds + i * kSimBytes, w[i], true);
         }
 #pragma unroll
-        for (int q = 0; q < kPartsDx; ++q) put_piece(lds + (2 + q) * kSimBytes, d[q], false);
+        for (int q = 0; q < kPartsDx; ++q) put_piece(part(q), d[q], false);
         __syncthreads();
         if (s + 1 < steps) load(s + 1);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            bf16x8_t fa[4], fb[kPartsDx][2];
+            if (s * kSim + ks * 32 >= a.E) break;
+            bf16x8_t fa[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) fa[i] = sim_frag<true>(lds + (wave & 1) * kSimBytes, 16 * i, ks, lane);
 #pragma unroll
-            for (int q = 0; q < kPartsDx; ++q)
+            for (int q = 0; q < kPartsDx; ++q) {
+                bf16x8_t fb[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    fb[q][j] = sim_frag<false>(lds + (2 + q) * kSimBytes, (wave >> 1) * 32 + 16 * j, ks, lane);
-#pragma unroll
-            for (int q = 0; q < kPartsDx; ++q)
+                for (int j = 0; j < 2; ++j) fb[j] = sim_frag<false>(part(q), (wave >> 1) * 32 + 16 * j, ks, lane);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[q][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+            }
         }
         __syncthreads();
     }
@@ -175,23 +227,22 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
     constexpr bool ANY = W != Widths::kWhole;
     const int c = tid % 16, col = k0 + c * 8, n = ANY ? min(V, a.K - col) : V;
     if (col >= a.K) return;
+    const int first = tid / 16;
     float f[4][V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int token = i * 16 + tid / 16;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + at(token, 2 * c + h));
+        for (int u = 0; u < 2; ++u) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(lds + at(first + i * 16, 2 * c + u));
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f[i][4 * h + u] = v[u];
+            for (int x = 0; x < 4; ++x) f[i][4 * u + x] = v[x];
         }
-    }
 #pragma unroll 2
     for (int j = 0; j < a.rows; ++j) {
         u16x8_t r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // (tokens past the last: the last one's, not stored)
-            const size_t t = t0 + min((long)(i * 16 + tid / 16), rows - 1);
+            const size_t t = t0 + min((long)(first + i * 16), rows - 1);
             r[i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n);
         }
 #pragma unroll
@@ -200,23 +251,22 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
             for (int u = 0; u < V; ++u) f[i][u] += bf16_bits_to_f32(r[i][u]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int token = i * 16 + tid / 16;
-        if (token < rows) st_bf16<ANY, true>(a.dx + (t0 + token) * a.K + col, n, f[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+        if (first + i * 16 < rows) st_bf16<ANY, true>(a.dx + (t0 + first + i * 16) * a.K + col, n, f[i]);
 }
 
 // ---- dWr ----------------------------------------------------------------------
-// 64 experts x 128 columns a workgroup over a range of the tokens.  One range
-// writes the results, more leave [range][E][ld] with the bias' sums behind a row.
+// 64 experts x 128 columns a workgroup over a range of the tokens; the waves take 32
+// x 64.  One range writes the results, more leave [range][E][ld] with the bias' sums
+// behind a row.
 __host__ __device__ inline int router_ld(int K) { return (K + 3) / 4 * 4 + 4; }
 
-template <Widths W>
+template <Widths W, bool IN_PLACE>
 __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uint16_t* __restrict__ parts, int splits,
                                                float* __restrict__ sums, int tile, char* lds) {
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols, Ep = router_ep(a.E), e_tiles = Ep / kSim;
+    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols, e_tiles = (a.E + kSim - 1) / kSim;
     int b = tile;
     const int e0 = b % e_tiles * kSim;
     b /= e_tiles;
@@ -228,17 +278,16 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-    float bias = 0.0f;  // of expert e0 + tid % 64, a quarter of a step's tokens
+    float bias = 0.0f;  // of expert e0 + tid % 64, a quarter of every step's tokens
     Piece x[2], d[kParts];
     auto load = [&](int s) {
         const size_t t0 = (size_t)(first + s) * kSim;
         const long rows = (long)a.M - (long)t0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) x[i] = get_piece<W>(a.x, t0, rows, a.K, k0 + i * kSim);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-            d[q] = get_piece<Widths::kWhole>(parts + (size_t)q * a.M * Ep, t0, rows, Ep, e0);
+        for (int i = 0; i < 2; ++i) x[i] = get_piece<W>(a.x + t0 * a.K, rows, a.K, k0 + i * kSim);
+        get_parts<kParts, IN_PLACE>(a, parts, t0, e0, d);
     };
+    auto part = [&](int q) { return lds + (2 + q) * kSimBytes; };
     if (steps > 0) load(0);
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
@@ -247,35 +296,37 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
             put_piece(lds + i * kSimBytes, x[i], true);
         }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) put_piece(lds + (2 + q) * kSimBytes, d[q], true);
+        for (int q = 0; q < kParts; ++q) put_piece(part(q), d[q], true);
         __syncthreads();
         if (s + 1 < steps) load(s + 1);
+        const int row0 = (wave >> 1) * 32;  // experts of the tile that the wave takes
+        if (e0 + row0 < a.E) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8_t fa[4], fb[kParts][2];
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8_t fa[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i] = sim_frag<true>(lds + (wave & 1) * kSimBytes, 16 * i, ks, lane);
+                for (int i = 0; i < 4; ++i) fa[i] = sim_frag<true>(lds + (wave & 1) * kSimBytes, 16 * i, ks, lane);
 #pragma unroll
-            for (int q = 0; q < kParts; ++q)
+                for (int q = 0; q < kParts; ++q) {
+                    bf16x8_t fb[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    fb[q][j] = sim_frag<true>(lds + (2 + q) * kSimBytes, (wave >> 1) * 32 + 16 * j, ks, lane);
+                    for (int j = 0; j < 2; ++j) fb[j] = sim_frag<true>(part(q), row0 + 16 * j, ks, lane);
 #pragma unroll
-            for (int q = 0; q < kParts; ++q)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[q][j], acc[i][j], 0, 0, 0);
+                        for (int j = 0; j < 2; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                }
+            }
         }
         if (a.dbias && k0 == 0) {
             const int e = tid % kSim;
-            for (int r = tid / kSim * 16; r < tid / kSim * 16 + 16; ++r) {
-                const char* p = lds + 2 * kSimBytes + sim_at<true>(r, e >> 3) + (e & 7) * 2;
+            for (int i = 0; i < kSim / 4; ++i) {
+                const int at = sim_at<true>(tid / kSim * (kSim / 4) + i, e >> 3) + (e & 7) * 2;
                 float v = 0.0f;
 #pragma unroll
                 for (int q = 0; q < kParts; ++q)  // exact: the parts of one fp32 number
-                    v += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p + q * kSimBytes));
+                    v += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(part(q) + at));
                 bias += v;
             }
         }
@@ -314,13 +365,14 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
 
 // Both products in one launch: dWr's tiles, which are bound by the matrix cores and
 // LDS, first, and dx's, which are bound by HBM, beside and behind them.
-template <Widths W>
-__global__ __launch_bounds__(256) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
-                                                              int splits, float* __restrict__ sums, int dw_tiles) {
+template <Widths W, bool IN_PLACE>
+__global__ __launch_bounds__(256, 3) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
+                                                                 int splits, float* __restrict__ sums, int dw_tiles) {
     __shared__ __attribute__((aligned(16))) char lds[(2 + kParts) * kSimBytes];
+    static_assert((2 + kParts) * kSimBytes >= kSim * kRouterCols * 4, "dx's tile in fp32 takes the pieces' place");
     const int b = (int)blockIdx.x;
-    if (b < dw_tiles) router_dw_tile<W>(a, parts, splits, sums, b, lds);
-    else router_dx_tile<W>(a, parts, b - dw_tiles, lds);
+    if (b < dw_tiles) router_dw_tile<W, IN_PLACE>(a, parts, splits, sums, b, lds);
+    else router_dx_tile<W, IN_PLACE>(a, parts, b - dw_tiles, lds);
 }
 
 // the ranges' sums in order, a thread per four values; the last four of a row: the bias
@@ -351,14 +403,22 @@ __global__ __launch_bounds__(256) void router_join_kernel(RouterBwdArgs a, int s
     }
 }
 
-// Ranges the tokens are cut into: until two workgroups a CU have one, as long as a
-// range keeps four steps.
-int router_splits(int M, int K, int E) {
-    const long tiles = (long)(router_ep(E) / kSim) * ((K + kRouterCols - 1) / kRouterCols);
+struct RouterPlan {
+    bool in_place;  // no launch for dl
+    int splits;     // ranges the tokens are cut into, for dWr
+    int k_tiles, dw_tiles, dx_tiles;
+};
+RouterPlan router_plan(int M, int K, int E) {
+    RouterPlan p;
+    p.in_place = M <= kSim && E <= kSim;
+    p.k_tiles = (K + kRouterCols - 1) / kRouterCols;
     const int steps = (M + kSim - 1) / kSim;
-    int splits = 1;
-    while (splits < 64 && tiles * splits * 2 <= 512 && steps / (splits * 2) >= 4) splits *= 2;
-    return splits;
+    const long tiles = (long)((E + kSim - 1) / kSim) * p.k_tiles;
+    p.splits = 1;
+    while (p.splits < 64 && tiles * p.splits * 2 <= 512 && steps / (p.splits * 2) >= 4) p.splits *= 2;
+    p.dw_tiles = (int)(tiles * p.splits);
+    p.dx_tiles = (int)((long)steps * p.k_tiles);
+    return p;
 }
 
 size_t parts_bytes(int M, int E) { return ((size_t)kParts * M * router_ep(E) * 2 + 255) / 256 * 256; }
@@ -366,44 +426,44 @@ size_t parts_bytes(int M, int E) { return ((size_t)kParts * M * router_ep(E) * 2
 }  // namespace
 
 long router_bwd_workgroups(int M, int K, int E) {
-    const long k_tiles = ((long)K + kRouterCols - 1) / kRouterCols;
-    const long dx = ((long)M + kSim - 1) / kSim * k_tiles;
-    const long dw = k_tiles * (router_ep(E) / kSim) * router_splits(M, K, E);
-    return dx + dw;
+    const RouterPlan p = router_plan(M, K, E);
+    return (long)p.k_tiles * ((M + kSim - 1) / kSim + p.splits * ((E + kSim - 1) / kSim));
 }
 
 size_t router_bwd_workspace(int M, int K, int E) {
-    const int splits = router_splits(M, K, E);
+    const int splits = router_plan(M, K, E).splits;
     return parts_bytes(M, E) + (splits > 1 ? (size_t)splits * E * router_ld(K) * 4 : 0);
 }
 
 void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {
     uint16_t* parts = (uint16_t*)workspace;
     float* sums = (float*)((char*)workspace + parts_bytes(a.M, a.E));
-    const int Ep = router_ep(a.E), splits = router_splits(a.M, a.K, a.E);
-    const int k_tiles = (a.K + kRouterCols - 1) / kRouterCols;
-    if (a.M > 0) {
+    const RouterPlan plan = router_plan(a.M, a.K, a.E);
+    if (a.M > 0 && !plan.in_place) {
         auto dl = [&](auto lanes) {
             constexpr int L = decltype(lanes)::value, tokens = 4 * (kWave / L);
             const int grid = (a.M + tokens - 1) / tokens;
             if (a.E % 4 == 0) router_dl_kernel<L, true><<<grid, 256, 0, s>>>(a, parts);
             else router_dl_kernel<L, false><<<grid, 256, 0, s>>>(a, parts);
         };
-        if (Ep == 64) dl(std::integral_constant<int, 16>{});
-        else if (Ep == 128) dl(std::integral_constant<int, 32>{});
+        if (a.E <= 64) dl(std::integral_constant<int, 16>{});
+        else if (a.E <= 128) dl(std::integral_constant<int, 32>{});
         else dl(std::integral_constant<int, 64>{});
     }
+    const int grid = plan.dw_tiles + plan.dx_tiles;
     auto products = [&](auto width) {
         constexpr Widths W = decltype(width)::value;
-        const int dw_tiles = k_tiles * (Ep / kSim) * splits, dx_tiles = (a.M + kSim - 1) / kSim * k_tiles;
-        router_products_kernel<W><<<dw_tiles + dx_tiles, 256, 0, s>>>(a, parts, splits, sums, dw_tiles);
+        if (plan.in_place)
+            router_products_kernel<W, true><<<grid, 256, 0, s>>>(a, parts, plan.splits, sums, plan.dw_tiles);
+        else
+            router_products_kernel<W, false><<<grid, 256, 0, s>>>(a, parts, plan.splits, sums, plan.dw_tiles);
     };
     if (a.K % 8 == 0) products(std::integral_constant<Widths, Widths::kWhole>{});
     else if (a.K >= 8) products(std::integral_constant<Widths, Widths::kLong>{});
     else products(std::integral_constant<Widths, Widths::kAny>{});
-    if (splits > 1) {
+    if (plan.splits > 1) {
         const long threads = (long)a.E * (router_ld(a.K) / 4);
-        router_join_kernel<<<(int)((threads + 255) / 256), 256, 0, s>>>(a, splits, sums);
+        router_join_kernel<<<(int)((threads + 255) / 256), 256, 0, s>>>(a, plan.splits, sums);
     }
 }
 
