@@ -278,7 +278,12 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-    float bias = 0.0f;  // of expert e0 + tid % 64, a quarter of every step's tokens
+    // the bias: the same product with a column of ones, 16 experts a wave
+    const bool with_bias = a.dbias && k0 == 0;
+    f32x4_t bias = {0, 0, 0, 0};
+    bf16x8_t ones;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ones[i] = 0x3f80;
     Piece x[2], d[kParts];
     auto load = [&](int s) {
         const size_t t0 = (size_t)(first + s) * kSim;
@@ -311,23 +316,14 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
                     bf16x8_t fb[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) fb[j] = sim_frag<true>(part(q), row0 + 16 * j, ks, lane);
+                    if (with_bias)
+                        bias = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, wave & 1 ? fb[1] : fb[0], bias, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
                 }
-            }
-        }
-        if (a.dbias && k0 == 0) {
-            const int e = tid % kSim;
-            for (int i = 0; i < kSim / 4; ++i) {
-                const int at = sim_at<true>(tid / kSim * (kSim / 4) + i, e >> 3) + (e & 7) * 2;
-                float v = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kParts; ++q)  // exact: the parts of one fp32 number
-                    v += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(part(q) + at));
-                bias += v;
             }
         }
         __syncthreads();
@@ -351,14 +347,11 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
             }
         }
     }
-    if (a.dbias && k0 == 0) {
-        float* q = reinterpret_cast<float*>(lds);
-        q[tid] = bias;
-        __syncthreads();
-        if (tid < kSim && e0 + tid < a.E) {
-            const float v = (q[tid] + q[tid + 64]) + (q[tid + 128] + q[tid + 192]);
-            if (splits > 1) out[(size_t)(e0 + tid) * ld + ld - 4] = v;
-            else a.dbias[e0 + tid] = v;
+    if (with_bias && lane < 16) {  // (every row of the product is the sum)
+        const int e = e0 + (wave >> 1) * 32 + (wave & 1) * 16 + lane;
+        if (e < a.E) {
+            if (splits > 1) out[(size_t)e * ld + ld - 4] = bias[0];
+            else a.dbias[e] = bias[0];
         }
     }
 }
