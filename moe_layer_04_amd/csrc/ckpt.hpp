@@ -70,33 +70,44 @@ __device__ __forceinline__ void ckpt_values(u32x2_t w, uint32_t X, float (&f)[V]
     for (int i = 0; i < V; ++i) f[i] = (float)(int8_t)(w[i / 4] >> (8 * (i % 4))) * step;
 }
 
-// n of 8 columns (ANY, ONCE: as in rows.hpp)
+// n of 8 columns' codes (ANY, ONCE, wide: as in rows.hpp)
 template <bool ANY, bool ONCE = false>
-__device__ __forceinline__ u32x2_t ld_codes(const int8_t* p, int n) {
-    u32x2_t w = {0, 0};
-    if constexpr (!ANY) {
-        if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
-        else return *reinterpret_cast<const u32x2_t*>(p);
-    } else if (n >= V) {
-        w = *reinterpret_cast<const u32x2_any_t*>(p);
+__device__ __forceinline__ u32x2_t ld_codes(const int8_t* p, int n, bool wide) {
+    if constexpr (!ANY && ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+    if constexpr (!ANY) return *reinterpret_cast<const u32x2_t*>(p);
+    if (n >= V) return *reinterpret_cast<const u32x2_any_t*>(p);
+    uint64_t b = 0;
+    if (wide) {
+        const int by = V - n;
+        b = __builtin_bit_cast(uint64_t, (u32x2_t)*reinterpret_cast<const u32x2_any_t*>(p - by)) >> (8 * by);
     } else {
 #pragma unroll
         for (int i = 0; i < V - 1; ++i)
-            if (i < n) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+            if (i < n) b |= (uint64_t)(uint8_t)p[i] << (8 * i);
     }
-    return w;
+    return __builtin_bit_cast(u32x2_t, b);
 }
-template <bool ANY, bool ONCE = false>
+template <bool ANY>
 __device__ __forceinline__ void st_codes(int8_t* p, int n, u32x2_t w) {
+    typedef uint32_t uint_any_t __attribute__((aligned(1)));
+    typedef uint16_t ushort_any_t __attribute__((aligned(1)));
     if constexpr (!ANY) {
-        if constexpr (ONCE) __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(p));
-        else *reinterpret_cast<u32x2_t*>(p) = w;
+        *reinterpret_cast<u32x2_t*>(p) = w;
     } else if (n >= V) {
         *reinterpret_cast<u32x2_any_t*>(p) = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V - 1; ++i)
-            if (i < n) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+    } else {  // as 4, 2 and 1 of them
+        uint32_t v = w[0];
+        if (n & 4) {
+            *reinterpret_cast<uint_any_t*>(p) = v;
+            p += 4;
+            v = w[1];
+        }
+        if (n & 2) {
+            *reinterpret_cast<ushort_any_t*>(p) = (uint16_t)v;
+            p += 2;
+            v >>= 16;
+        }
+        if (n & 1) *p = (int8_t)v;
     }
 }
 

@@ -243,7 +243,7 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // (tokens past the last: the last one's, not stored)
             const size_t t = t0 + min((long)(first + i * 16), rows - 1);
-            r[i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n);
+            r[i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n, a.K >= V);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -30,6 +30,23 @@ __device__ __forceinline__ void ld_bf16(const uint16_t* p, int n, float (&f)[V])
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = bf16_bits_to_f32(v[i]);
 }
+// the first n < 8 of 8 values, as 4, 2 and 1 of them
+__device__ __forceinline__ void st_part(uint16_t* p, int n, uint4 w) {
+    typedef uint2 uint2_any_t __attribute__((aligned(2)));
+    typedef uint32_t uint_any_t __attribute__((aligned(2)));
+    if (n & 4) {
+        *reinterpret_cast<uint2_any_t*>(p) = uint2{w.x, w.y};
+        p += 4;
+        w.x = w.z;
+        w.y = w.w;
+    }
+    if (n & 2) {
+        *reinterpret_cast<uint_any_t*>(p) = w.x;
+        p += 2;
+        w.x = w.y;
+    }
+    if (n & 1) *p = (uint16_t)w.x;
+}
 template <bool ANY, bool ONCE = false>
 __device__ __forceinline__ void st_bf16(uint16_t* p, int n, const float (&f)[V]) {
     u16x8_t v;
@@ -38,11 +55,7 @@ __device__ __forceinline__ void st_bf16(uint16_t* p, int n, const float (&f)[V])
     if constexpr (!ANY && ONCE) __builtin_nontemporal_store(v, reinterpret_cast<u16x8_t*>(p));
     else if constexpr (!ANY) *reinterpret_cast<u16x8_t*>(p) = v;
     else if (n >= V) *reinterpret_cast<u16x8_any_t*>(p) = v;
-    else {
-#pragma unroll
-        for (int i = 0; i < V - 1; ++i)
-            if (i < n) p[i] = v[i];
-    }
+    else st_part(p, n, __builtin_bit_cast(uint4, v));
 }
 template <bool ANY>
 __device__ __forceinline__ void ld_f32(const float* p, int n, float (&f)[V]) {
@@ -77,9 +90,10 @@ __device__ __forceinline__ void st_f32(float* p, int n, const float (&f)[V]) {
     }
 }
 
-// the bits of n of 8 columns of a row, zeros past them
+// The bits of n of 8 columns of a row, zeros past them.  wide: the row has 8
+// columns or more, and its last ones are loaded as its last 8 and moved into place.
 template <bool ANY, bool ONCE = false>
-__device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n) {
+__device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n, bool wide) {
     u16x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
     if constexpr (!ANY) {
         if (n <= 0) return v;
@@ -87,6 +101,14 @@ __device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n) {
         else return *reinterpret_cast<const u16x8_t*>(p);
     } else if (n >= V) {
         v = *reinterpret_cast<const u16x8_any_t*>(p);
+    } else if (wide && n > 0) {
+        const int by = V - n;  // elements to drop in front
+        uint4 w = __builtin_bit_cast(uint4, (u16x8_t)*reinterpret_cast<const u16x8_any_t*>(p - by));
+        if (by & 4) w = uint4{w.z, w.w, 0, 0};
+        if (by & 2) w = uint4{w.y, w.z, w.w, 0};
+        if (by & 1)
+            w = uint4{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
+        v = __builtin_bit_cast(u16x8_t, w);
     } else {
 #pragma unroll
         for (int i = 0; i < V - 1; ++i)
@@ -94,4 +116,11 @@ __device__ __forceinline__ u16x8_t ld_bf16_bits(const uint16_t* p, int n) {
     }
     return v;
 }
+template <bool ANY, bool ONCE = false>
+__device__ __forceinline__ void ld_bf16(const uint16_t* p, int n, bool wide, float (&f)[V]) {
+    const u16x8_t v = ld_bf16_bits<ANY, ONCE>(p, n, wide);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = bf16_bits_to_f32(v[i]);
+}
+
 }  // namespace moe
