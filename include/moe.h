@@ -564,7 +564,8 @@ moe_status moe_silu_mul_bwd(const void *da, const void *g, const float *topk_wei
  *   a          moe_silu_mul_bwd_ckpt: out bf16 [R,N], or NULL
  *   the rest   as the operators of the same names.  Padding rows are kept as
  *              zeros; rows at and past num_rows stay as they are.  The workspace of
- *              moe_grouped_gemm_dw_ckpt depends on the same sizes and is always used.
+ *              moe_grouped_gemm_dw_ckpt depends on the same sizes; it holds x
+ *              in bf16 where a product reads it more often than a few times.
  *
  * Outputs must not overlap an input or one another (INVALID_ARG).
  *

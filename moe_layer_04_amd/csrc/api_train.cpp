@@ -26,6 +26,8 @@ moe_status grouped_setup(moe::GroupedArgs* g, const int32_t* offsets, const int3
     if (wide * (R / 64 + (long)E) >= most || (long)E * ((K + 63) / 64) * ((N + 63) / 64) >= most)
         return MOE_ERR_UNSUPPORTED;
     g->w = g->x = g->dy = nullptr;
+    g->codes = nullptr;
+    g->scales = nullptr;
     g->offsets = offsets;
     g->sorted = sorted_ids;
     g->how_x = g->how_dy = g->how_out = moe::kRowSorted;
@@ -101,8 +103,8 @@ MOE_API moe_status moe_grouped_gemm_dx(const void* dy, const void* w,
 }
 
 namespace {
-// dw, with x as bf16 rows or (scales given) as rows kept in 8 bits, which are
-// brought back to bf16 in the workspace, before the product's own
+// dw, with x as bf16 rows or as rows kept in 8 bits, which the large tiles need
+// brought back to bf16: in the workspace, before the product's own
 moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* scales,
                       const int32_t* expert_offsets, const int32_t* sorted_ids, int rows, int T,
                       int topk, int R, int E, int K, int N, int out, void* dw, void* workspace,
@@ -122,7 +124,7 @@ moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* s
     g.out_f32 = out != MOE_OUT_BF16;
     g.accumulate = out == MOE_OUT_FP32_ADD;
     size_t need = used_size(moe::grouped_dw_workspace(g));
-    const size_t restored = kept ? round_up((size_t)x_rows * K * 2) : 0;
+    const size_t restored = kept && grouped_dw_restores(g) ? round_up((size_t)x_rows * K * 2) : 0;
     if (restored) need = restored + (need < kAlign ? kAlign : need);
     if (workspace_step(workspace, workspace_bytes, need, &st)) return st;
     if (R == 0 && g.accumulate) return MOE_OK;
@@ -139,13 +141,19 @@ moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* s
         (kept && overlap(dw, dw_bytes, scales, x_rows * ckpt_blocks(K))))
         return MOE_ERR_INVALID_ARG;
     g.dy = (const uint16_t*)dy;
-    g.x = (const uint16_t*)x;
+    if (kept) {
+        g.codes = (const int8_t*)x;
+        g.scales = scales;
+    } else {
+        g.x = (const uint16_t*)x;
+    }
     g.how_x = rows & MOE_ROWS_GATHER ? moe::kRowToken : moe::kRowSorted;
     g.how_dy = rows & MOE_ROWS_GATHER_DY ? moe::kRowToken : moe::kRowSorted;
     g.out = dw;
     (void)hipGetLastError();
-    if (restored && R > 0) {
+    if (restored) {
         g.x = (const uint16_t*)workspace;
+        g.codes = nullptr;
         moe::launch_ckpt_restore((const int8_t*)x, scales, (int)x_rows, K, (uint16_t*)workspace,
                                  (hipStream_t)stream);
     }

@@ -11,6 +11,7 @@
 // neighbours in memory) and "B" (the other one).  Row lookups (gather by
 // token, scatter by slot) happen in the kernels; sums are fp32.
 #include "../../include/moe.h"
+#include "ckpt.hpp"
 #include "grouped.hpp"
 #include "small_tiles.hpp"
 #include "tiles.hpp"
@@ -95,8 +96,54 @@ __device__ __forceinline__ void store_grad(char* lds, const f32x4_t (&acc)[TILE 
     }
 }
 
-template <int OP, Widths W, int TILE>
-__global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void grouped_small_kernel(
+// A chunk of x kept in 8 bits, loaded and settled as one of bf16 (load_chunk); its
+// values are formed when it is stored.
+struct KeptChunk {
+    u32x2_t codes;
+    uint32_t X;
+};
+template <Widths W>
+__device__ __forceinline__ KeptChunk load_kept(const GroupedArgs& g, int row, int c) {
+    const bool in = row >= 0 && c < g.K;
+    const int8_t* zeros = reinterpret_cast<const int8_t*>(kZeros);
+    const int8_t* codes = in ? g.codes + (size_t)row * g.K : zeros;
+    const uint8_t* scale = in ? g.scales + (size_t)row * ckpt_blocks(g.K) + c / kCkptBlock
+                              : reinterpret_cast<const uint8_t*>(zeros);
+    typedef const __attribute__((address_space(1))) uint8_t* global_scale_t;
+    KeptChunk v;
+    v.X = *(global_scale_t)(uintptr_t)scale;
+    if constexpr (W == Widths::kWhole) {
+        typedef const __attribute__((address_space(1))) u32x2_t* global_t;
+        v.codes = *(global_t)(uintptr_t)(codes + (in ? c : 0));
+    } else if (W == Widths::kAny && g.K < 8) {
+        uint64_t b = 0;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (in && c + i < g.K) b |= (uint64_t)(uint8_t)codes[c + i] << (8 * i);
+        v.codes = __builtin_bit_cast(u32x2_t, b);
+    } else {
+        typedef const __attribute__((address_space(1))) u32x2_any_t* global_t;
+        v.codes = *(global_t)(uintptr_t)(codes + (in ? min(c, g.K - 8) : 0));
+    }
+    return v;
+}
+using moe::settle_chunk;
+__device__ __forceinline__ KeptChunk settle_chunk(KeptChunk v, int c, int width) {
+    const int by = width < 8 ? 0 : min(max(c - (width - 8), 0), 7);  // (8 and more: no columns, zeros)
+    v.codes = __builtin_bit_cast(u32x2_t, __builtin_bit_cast(uint64_t, v.codes) >> (8 * by));
+    return v;
+}
+__device__ __forceinline__ u16x8_t chunk_bits(u16x8_t v) { return v; }
+__device__ __forceinline__ u16x8_t chunk_bits(KeptChunk v) {
+    float f[V];
+    ckpt_values(v.codes, v.X, f);
+    const uint4 w = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                     pack_bf16x2(f[6], f[7])};
+    return __builtin_bit_cast(u16x8_t, w);
+}
+
+template <int OP, Widths W, int TILE, bool KEPT>
+__global__ __launch_bounds__(256, TILE > kSim || KEPT ? 2 : OP == kOpDw ? 3 : 4) void grouped_small_kernel(
     GroupedArgs g) {
     constexpr bool ACOL = OP != kOpFwd, BCOL = OP == kOpDw;
     constexpr int AHEAD = TILE > kSim && OP == kOpDw ? 1 : kSimAhead;
@@ -158,7 +205,11 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
             if (row >= 0) brow[h] = (OP == kOpFwd ? g.x : g.dy) + (size_t)row * red;
         }
     }
-    struct Step { u16x8_t a[H], b[H]; };
+    typedef typename std::conditional<KEPT, KeptChunk, u16x8_t>::type chunk_a_t;
+    struct Step {
+        chunk_a_t a[H];
+        u16x8_t b[H];
+    };
     auto load = [&](int step) {
         Step s;
         const int r0 = step * kSim;
@@ -181,7 +232,8 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int x = rx[h & 1], y = ry[h & 1];
-                s.a[h] = load_chunk<W>(x < 0 ? nullptr : g.x + (size_t)x * g.K, a0 + col_at(h), g.K);
+                if constexpr (KEPT) s.a[h] = load_kept<W>(g, x, a0 + col_at(h));
+                else s.a[h] = load_chunk<W>(x < 0 ? nullptr : g.x + (size_t)x * g.K, a0 + col_at(h), g.K);
                 s.b[h] = load_chunk<W>(y < 0 ? nullptr : g.dy + (size_t)y * g.N, b0 + col_at(h), g.N);
             }
         } else {
@@ -242,7 +294,7 @@ __global__ __launch_bounds__(256, TILE > kSim ? 2 : OP == kOpDw ? 3 : 4) void gr
             for (int h = 0; h < H; ++h) {
                 // the h/2-th 64 rows or columns
                 char* to = buf + (h >> 1) * kSimBytes;
-                *reinterpret_cast<u16x8_t*>(to + sim_at<ACOL>(col_row(h), c)) = ahead[i].a[h];
+                *reinterpret_cast<u16x8_t*>(to + sim_at<ACOL>(col_row(h), c)) = chunk_bits(ahead[i].a[h]);
                 *reinterpret_cast<u16x8_t*>(to + kOperand + sim_at<BCOL>(col_row(h), c)) = ahead[i].b[h];
             }
             // the buffer written next was last read before this barrier
@@ -341,7 +393,14 @@ int small_workgroups(const GroupedArgs& g, int op, int tile) {
 }
 template <int OP, Widths W, int TILE>
 void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
-    grouped_small_kernel<OP, W, TILE><<<small_workgroups(g, OP, TILE), 256, 0, s>>>(g);
+    const int grid = small_workgroups(g, OP, TILE);
+    if constexpr (OP == kOpDw && TILE == kSim) {
+        if (g.codes) {
+            grouped_small_kernel<OP, W, TILE, true><<<grid, 256, 0, s>>>(g);
+            return;
+        }
+    }
+    grouped_small_kernel<OP, W, TILE, false><<<grid, 256, 0, s>>>(g);
 }
 // Rows that are no whole chunks, with enough of them and enough outputs, on 128
 // x 128 tiles: half the loads an output.  us, 64 / 128, T tokens x k over E
@@ -548,6 +607,14 @@ void launch_grouped_dx(const GroupedArgs& g, void* workspace, hipStream_t s) {
 size_t grouped_dw_workspace(const GroupedArgs& g) {
     const int splits = small_dw(g) ? 1 : grouped_tiles_dw_splits(g);
     return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;
+}
+// x kept in 8 bits: few small tiles form its values as they store them to LDS, each
+// its own; with more of them a launch that brings the rows back costs less.  us,
+// so / brought back: 666 rows over 8 experts of 1032 x 256 [544 tiles] 9.6/11.0, 1000
+// over 7 of 1001 x 330 [672] 11.2/13.7, 512 of one 512 x 512 [64] 12.6/13.9; 1024 over
+// 8 of 1024 x 1024 [2048] 22.7/20.1, 4096 over 8 of 4097 x 2049 (128 x 128) 356/320
+bool grouped_dw_restores(const GroupedArgs& g) {
+    return !small_dw(g) || wide(g, kOpDw) || small_workgroups(g, kOpDw, kSim) > 1024;
 }
 void launch_grouped_dw(const GroupedArgs& call, void* workspace, hipStream_t s) {
     GroupedArgs g = call;

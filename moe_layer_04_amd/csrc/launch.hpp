@@ -169,6 +169,8 @@ constexpr uint32_t kRowToken = 1;   // row sorted[i] / topk
 constexpr uint32_t kRowSlot = 2;    // row sorted[i]
 struct GroupedArgs {
     const uint16_t *w, *x, *dy;  // w [E,N,K]; x rows of K, dy rows of N (dw: no w; fwd: no dy; dx: no x)
+    const int8_t* codes;         // dw: x kept in 8 bits (then no x), and its scales; or null
+    const uint8_t* scales;
     const int32_t* offsets;      // [E+1], device
     const int32_t* sorted;       // [R] slots, or null
     uint32_t how_x, how_dy, how_out;
@@ -197,6 +199,8 @@ void launch_grouped_tiles_dx(const GroupedArgs& g, hipStream_t s);
 int grouped_tiles_dw_splits(const GroupedArgs& g);
 void launch_grouped_tiles_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
 size_t grouped_dw_workspace(const GroupedArgs& g);
+// whether x kept in 8 bits has to be brought back to bf16 before launch_grouped_dw
+bool grouped_dw_restores(const GroupedArgs& g);
 void launch_grouped_dw(const GroupedArgs& g, void* workspace, hipStream_t s);
 
 // ---- the gated activation between the products (gated_act.hip) ------------------

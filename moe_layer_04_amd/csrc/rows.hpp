@@ -32,10 +32,9 @@ __device__ __forceinline__ void ld_bf16(const uint16_t* p, int n, float (&f)[V])
 }
 // the first n < 8 of 8 values, as 4, 2 and 1 of them
 __device__ __forceinline__ void st_part(uint16_t* p, int n, uint4 w) {
-    typedef uint2 uint2_any_t __attribute__((aligned(2)));
     typedef uint32_t uint_any_t __attribute__((aligned(2)));
     if (n & 4) {
-        *reinterpret_cast<uint2_any_t*>(p) = uint2{w.x, w.y};
+        *reinterpret_cast<u16x4_any_t*>(p) = __builtin_bit_cast(u16x4_t, uint2{w.x, w.y});
         p += 4;
         w.x = w.z;
         w.y = w.w;

@@ -296,9 +296,11 @@ def test_refusals(moe):
                  lambda: moe.moe_grouped_gemm_dw_ckpt(x, codes, X, off, accumulate=True)):
         with pytest.raises(ValueError):
             call()
+    # large tiles need the rows brought back in the workspace
     small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    big, off = bf16((4096, 512), 3), torch.tensor([0, 4096], dtype=torch.int32, device="cuda")
     with pytest.raises(moe.MoEError):
-        moe.moe_grouped_gemm_dw_ckpt(x, codes, X, off, workspace=small)
+        moe.moe_grouped_gemm_dw_ckpt(big, *moe.moe_ckpt_rows(big), off, workspace=small)
     with pytest.raises(moe.MoEError):            # the output over the codes
         moe.moe_ckpt_restore(codes.view(-1)[:64].view(2, 32), X.view(-1)[:2].view(2, 1),
                              out=codes.view(-1)[32:160].view(torch.bfloat16).view(2, 32))
