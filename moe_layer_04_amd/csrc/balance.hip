@@ -23,6 +23,16 @@ namespace {
 constexpr int kSplit = 4;     // experts of a group
 constexpr int kGroups = 256;  // workgroups of the forward at most: one a CU
 
+// e^d for d <= 0 or NaN: 2^t with t = d log2 e, whose rounding is made good by the
+// first term of its effect (2^t alone is off by |d| half steps)
+__device__ __forceinline__ float exp_below(float d) {
+    d = d < -150.0f ? -150.0f : d;
+    const float t = d * 1.44269502f;
+    const float rest = fmaf(d, 1.92596303e-8f, fmaf(d, 1.44269502f, -t));  // log2 e = 1.44269502 + 1.926e-8
+    const float p = __builtin_amdgcn_exp2f(t);
+    return fmaf(p, rest * 0.693147182f, p);
+}
+
 // experts of a token's lane: groups of four, 4 * L apart
 template <int L, int C, bool VEC>
 struct Token {
@@ -72,7 +82,7 @@ struct Token {
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int i = 0; i < kSplit; ++i) v[c][i] = __expf(v[c][i] - base);
+            for (int i = 0; i < kSplit; ++i) v[c][i] = exp_below(v[c][i] - base);
         const float s = sum([&](int c, int i) { return v[c][i]; });
         const float r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
 #pragma unroll
