@@ -117,7 +117,7 @@ def moe_topk_bwd(x: torch.Tensor, w_router: torch.Tensor, topk_ids: Optional[tor
             raise ValueError(f"dx_rows must have a multiple of {M} rows, got {count}")
         _arg(dx_rows, "dx_rows", _BF16, (count, K), dev)
     need = _topk_bwd_workspace(rows, M, K, E, topk)
-    workspace = _workspace(dev, workspace, need)
+    workspace = _workspace(dev, workspace, need, True)
     dx, dw = _new(_BF16, dev, M, K), _new(_F32, dev, E, K)
     dbias = _new(_F32, dev, E) if bias else None
     _call(dev, "moe_topk_bwd", _p(x), _p(w_router), _p(topk_ids), _p(topk_weights), _p(dtopk_weights),

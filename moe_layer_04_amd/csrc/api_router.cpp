@@ -87,7 +87,7 @@ MOE_API moe_status moe_topk_bwd(const void* x, const void* w_router, const int32
     if (K >= kMaxWidth || rows > MOE_MAX_TOPK || (long)M * rows >= kMaxRows ||
         router_bwd_workgroups(M, K, E) * 256 >= kMaxThreads)
         return MOE_ERR_UNSUPPORTED;
-    if (workspace_step(workspace, workspace_bytes, round_up(router_bwd_workspace(M, K, E)), &st)) return st;
+    if (workspace_step(workspace, workspace_bytes, used_size(router_bwd_workspace(M, K, E)), &st)) return st;
     if (!dw) return MOE_ERR_INVALID_ARG;
     if (M > 0) {
         if (!x || !w_router || !dx || !dx_rows != !rows) return MOE_ERR_INVALID_ARG;

@@ -424,8 +424,9 @@ long router_bwd_workgroups(int M, int K, int E) {
 }
 
 size_t router_bwd_workspace(int M, int K, int E) {
-    const int splits = router_plan(M, K, E).splits;
-    return parts_bytes(M, E) + (splits > 1 ? (size_t)splits * E * router_ld(K) * 4 : 0);
+    const RouterPlan plan = router_plan(M, K, E);
+    const int splits = plan.splits;
+    return plan.in_place ? 0 : parts_bytes(M, E) + (splits > 1 ? (size_t)splits * E * router_ld(K) * 4 : 0);
 }
 
 void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {

@@ -90,10 +90,13 @@ def test_topk_bwd_refusals(lib):
     for kw in (*BIG, dict(K=1 << 20), dict(rows=17), dict(M=1 << 25, rows=16, topk=1), dict(M=1 << 24, K=1 << 14)):
         assert call(**kw) == UNS, kw
     query = {k: None for k in names}
-    assert call(**query) == OK
-    need = n.value
-    assert need >= 3 * 16 * 64 * 2 and need % 256 == 0
-    assert call(nbytes=need - 1) == WSP
+    assert call(**query) == OK and n.value == 256              # few tokens and experts: not used
+    assert call(nbytes=255) == WSP
+    for kw in (dict(M=65), dict(E=65)):
+        assert call(**query, **kw) == OK
+        need = n.value
+        assert need >= 3 * 16 * 64 * 2 and need % 256 == 0
+        assert call(nbytes=need - 1, **kw) == WSP
     # the tokens in ranges: their sums
     assert call(**query, M=4096) == OK and n.value > 3 * 4096 * 64 * 2
     size = dict(x=2048, w=1024, ids=128, wts=128, dwts=128, dl=512, more=4096, dx=2048, dw=2048, db=32)
