@@ -403,9 +403,10 @@ struct RouterPlan {
 };
 RouterPlan router_plan(int M, int K, int E) {
     RouterPlan p;
-    // us of the GPU, formed in place / by a launch of its own: 64 tokens of 256 over 8
-    // experts 5.6/6.5, 256 of 4096 over 8 18.7/11.5 (and a launch is 3.4 us of the host)
-    p.in_place = M <= kSim && E <= kSim;
+    // us a call, formed in place / by a launch of its own: 64 tokens of 4096 over 8
+    // experts 13.0/17, 128 of 4096 over 8 13.4/17.1, of 1024 over 64 16.1/16.8, 190 of
+    // 4096 over 64 22.6/16.8, 64 of 1024 over 128 17.1/16.7
+    p.in_place = M <= 2 * kSim && E <= kSim;
     p.k_tiles = (K + kRouterCols - 1) / kRouterCols;
     const int steps = (M + kSim - 1) / kSim;
     const long tiles = (long)((E + kSim - 1) / kSim) * p.k_tiles;

@@ -330,7 +330,7 @@ def test_refusals(moe):
                  lambda: moe.moe_balance(f32((4, 257), 1), ids),
                  lambda: moe.moe_balance_bwd(loss, logits, counts, tokens, 9),
                  lambda: moe.moe_topk_bwd(**{**s, "dx_rows": bf16((4 * 17, 16), 1)}),
-                 lambda: moe.moe_topk_bwd(**inputs(70, 16, 8, 2, 2, True, True, 1),
+                 lambda: moe.moe_topk_bwd(**inputs(140, 16, 8, 2, 2, True, True, 1),
                                           workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(moe.MoEError):
             call()

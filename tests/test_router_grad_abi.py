@@ -92,7 +92,7 @@ def test_topk_bwd_refusals(lib):
     query = {k: None for k in names}
     assert call(**query) == OK and n.value == 256              # few tokens and experts: not used
     assert call(nbytes=255) == WSP
-    for kw in (dict(M=65), dict(E=65)):
+    for kw in (dict(M=129), dict(E=65)):
         assert call(**query, **kw) == OK
         need = n.value
         assert need >= 3 * 16 * 64 * 2 and need % 256 == 0
