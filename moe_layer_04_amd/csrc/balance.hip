@@ -84,7 +84,8 @@ struct Token {
 #pragma unroll
             for (int i = 0; i < kSplit; ++i) v[c][i] = exp_below(v[c][i] - base);
         const float s = sum([&](int c, int i) { return v[c][i]; });
-        const float r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);
+        float r = __builtin_amdgcn_rcpf(s);
+        r = s == 0.0f ? 0.0f : fmaf(fmaf(-s, r, 1.0f), r, r);  // within half a step
 #pragma unroll
         for (int c = 0; c < C; ++c) v[c] *= r;
     }
@@ -92,11 +93,10 @@ struct Token {
 
 // counts and probs of expert e from the sums of all tokens; its share of the loss / E
 __device__ __forceinline__ float balance_expert(const BalanceArgs& a, int e, float psum, int count, int n) {
-    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    const float P = psum * inv;
+    const float P = n > 0 ? psum / (float)n : 0.0f;
     a.counts[e] = count;
     a.probs[e] = P;
-    return (float)count * inv / (float)a.topk * P;
+    return n > 0 ? (float)count / ((float)n * (float)a.topk) * P : 0.0f;
 }
 
 // Sums of many workgroups, in the workspace: [groups][E] of p, [groups][E] of
