@@ -364,8 +364,15 @@ __global__ __launch_bounds__(256, 3) void router_products_kernel(RouterBwdArgs a
     __shared__ __attribute__((aligned(16))) char lds[(2 + kParts) * kSimBytes];
     static_assert((2 + kParts) * kSimBytes >= kSim * kRouterCols * 4, "dx's tile in fp32 takes the pieces' place");
     const int b = (int)blockIdx.x;
-    if (b < dw_tiles) router_dw_tile<W, IN_PLACE>(a, parts, splits, sums, b, lds);
-    else router_dx_tile<W, IN_PLACE>(a, parts, b - dw_tiles, lds);
+    // (the hardware deals workgroup g to XCD g % 8: an XCD takes neighbouring tiles
+    // of dWr, whose tokens its L2 then holds for all of a column's experts)
+    const int per_xcd = (dw_tiles + 7) / 8;
+    if (b < 8 * per_xcd) {
+        const int tile = b % 8 * per_xcd + b / 8;
+        if (tile < dw_tiles) router_dw_tile<W, IN_PLACE>(a, parts, splits, sums, tile, lds);
+    } else {
+        router_dx_tile<W, IN_PLACE>(a, parts, b - 8 * per_xcd, lds);
+    }
 }
 
 // the ranges' sums in order, a thread per four values; the last four of a row: the bias
@@ -427,7 +434,7 @@ size_t parts_bytes(int M, int E) { return ((size_t)kParts * M * router_ep(E) * 2
 
 long router_bwd_workgroups(int M, int K, int E) {
     const RouterPlan p = router_plan(M, K, E);
-    return (long)p.k_tiles * ((M + kSim - 1) / kSim + p.splits * ((E + kSim - 1) / kSim));
+    return (long)p.k_tiles * ((M + kSim - 1) / kSim + p.splits * ((E + kSim - 1) / kSim)) + 7;
 }
 
 size_t router_bwd_workspace(int M, int K, int E) {
@@ -451,7 +458,7 @@ void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {
         else if (a.E <= 128) dl(std::integral_constant<int, 32>{});
         else dl(std::integral_constant<int, 64>{});
     }
-    const int grid = plan.dw_tiles + plan.dx_tiles;
+    const int grid = (plan.dw_tiles + 7) / 8 * 8 + plan.dx_tiles;
     auto products = [&](auto width) {
         constexpr Widths W = decltype(width)::value;
         if (plan.in_place)
