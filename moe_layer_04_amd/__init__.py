@@ -3,8 +3,9 @@
 The layer -- top-k softmax router, expert-sorted token permutation, grouped
 expert GEMMs with a fused SiLU*up epilogue, weighted un-permute combine --
 runs in hand-written HIP kernels behind the C ABI of include/moe.h
-(libmoe.so), as one call or in pieces with their gradients; this package is its thin ctypes binding plus the seeded input
-generator used by tests and benchmarks.
+(libmoe.so), as one call or in pieces with their gradients, the router's balance
+loss and gradients and activations kept in 8 bits; this package is its thin
+ctypes binding plus the seeded input generator used by tests and benchmarks.
 """
 from ._binding import (MOE_BF16, FusedForwardGraph, MOE_ERR_HIP, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED,
                        MOE_ERR_WORKSPACE, MOE_FP8_E4M3, MOE_FP8_E4M3_ROWWISE, MOE_MXFP4_E2M1, MOE_OK, MOE_REGIME_AUTO,

@@ -10,7 +10,9 @@
 // cost is shared by them.  Both passes are meant to be bound by HBM: the logits are
 // read once, as 16 bytes a lane and group.  Sums are fp32 in a fixed order: a
 // lane's tokens one after the other, then the lanes, the waves and the workgroups;
-// counts are integers.
+// counts are integers.  32768 tokens of 256 experts: forward 8.9 us (35 MB; 13.1 with
+// 64 lanes a token, whose exchanges it then waits for) and 4.2 to join the
+// workgroups, backward 12.4 us (67 MB, 5.4 TB/s).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -270,8 +272,10 @@ __global__ __launch_bounds__(kJoinExperts* kJoinSlices) void balance_join_kernel
     a.loss[0] = (float)a.E * loss;
 }
 
-// (The logits of a token that does not count may be anything: its gradient is
-// written as zeros whatever was computed.)
+// A wave's next tokens are loaded before the present ones are worked on, and results
+// do not stay in the L2 (32768 x 256: 12.4 us, 15.5 in ordinary stores; 2048
+// workgroups, which go around once, 16.7).  (The logits of a token that does not
+// count may be anything: its gradient is written as zeros whatever was computed.)
 constexpr int kBwdGroups = 1024;  // workgroups at most
 
 template <int L, int C, bool VEC>

@@ -10,6 +10,10 @@
 // it left: two parts hold 16 bits of it, three all 24, and the products run on the
 // bf16 matrix cores with sums in fp32.  dx, which is rounded to bf16 itself, takes
 // two (off by at most 2^-16 of a term), dWr three, so nothing of dl is lost in it.
+// Bound by HBM with few experts, with many by the latency of dWr's steps, whose
+// workgroups are few: 4096 tokens of 4096 over 8 experts, two rows a token, 28 us
+// for the products (134 MB), 4 for dl and 4 to join dWr's ranges; of 7168 over 256
+// and eight rows 151 us (587 MB; dx alone 116, dWr alone 60), 6 and 6.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "small_tiles.hpp"
@@ -356,8 +360,9 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
     }
 }
 
-// Both products in one launch: dWr's tiles, which are bound by the matrix cores and
-// LDS, first, and dx's, which are bound by HBM, beside and behind them.
+// Both products in one launch: dWr's tiles, which take long and wait for their steps,
+// first, and dx's, which are bound by HBM, beside and behind them (4096 x 7168 over
+// 256: 163 us a call, dx's first 186).
 template <Widths W, bool IN_PLACE>
 __global__ __launch_bounds__(256, 3) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
                                                                  int splits, float* __restrict__ sums, int dw_tiles) {
