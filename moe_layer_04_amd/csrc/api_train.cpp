@@ -151,7 +151,7 @@ moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* s
     g.how_dy = rows & MOE_ROWS_GATHER_DY ? moe::kRowToken : moe::kRowSorted;
     g.out = dw;
     (void)hipGetLastError();
-    if (restored) {
+    if (restored && R > 0) {  // (without rows nothing is read, and the codes may be null)
         g.x = (const uint16_t*)workspace;
         g.codes = nullptr;
         moe::launch_ckpt_restore((const int8_t*)x, scales, (int)x_rows, K, (uint16_t*)workspace,

@@ -219,8 +219,8 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a,
     }
 }
 
-// The workgroups' sums in order, 32 experts a workgroup and 32 threads an
-// expert.  The workgroup that is done last adds up the shares of the loss, in the
+// The workgroups' sums, 32 experts a workgroup and 32 threads an expert, in an order
+// of their own.  The workgroup that is done last adds up the shares of the loss, in the
 // order of the experts whichever it is.  (One workgroup for all of 256 experts
 // is bound by what a CU can load: 7.0 us of 256 groups' sums.)
 __global__ __launch_bounds__(kJoinExperts* kJoinSlices) void balance_join_kernel(BalanceArgs a, int groups,

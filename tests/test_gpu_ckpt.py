@@ -270,6 +270,25 @@ def test_dw_without_rows(moe):
     assert (got == 0).all()
 
 
+@pytest.mark.parametrize("E,N,K", [(3, 24, 40), (2, 2051, 1030), (16, 1024, 1024)])
+def test_dw_without_rows_reads_nothing(moe, E, N, K):
+    """R == 0 with tokens and no tensors of rows: null operands, zeros written."""
+    note(f"dw_ckpt R=0, null operands, {E} x {N} x {K}")
+    import ctypes
+    lib = moe.load_library()
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    dw = torch.full((E, N, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    n = ctypes.c_size_t(0)
+    sizes = (1, 8, 2, 0, E, K, N, 0)
+    assert lib.moe_grouped_gemm_dw_ckpt(*[None] * 5, *sizes, None, None, ctypes.byref(n), None) == 0
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    assert lib.moe_grouped_gemm_dw_ckpt(None, None, None, off.data_ptr(), None, *sizes, dw.data_ptr(),
+                                        ws.data_ptr(), ctypes.byref(n),
+                                        torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert (dw == 0).all()
+
+
 # --------------------------------------------------------------------------
 # refusals, streams, graphs
 # --------------------------------------------------------------------------
