@@ -188,6 +188,24 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
     };
     auto part = [&](int q) { return lds + (2 + q) * kSimBytes; };
     load(0);
+    // four groups of 8 columns a thread, 16 tokens apart; the first rows to be added
+    // are on their way while the products are formed
+    constexpr bool ANY = W != Widths::kWhole;
+    const int c = tid % 16, col = k0 + c * 8, n = ANY ? min(V, a.K - col) : V, first = tid / 16;
+    u16x8_t row[2][4];
+    auto load_rows = [&](auto at, int j) {
+        constexpr int J = decltype(at)::value;
+        if (col >= a.K || j >= a.rows) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // (tokens past the last: the last one's, not stored)
+            const size_t t = t0 + min((long)(first + i * 16), rows - 1);
+            row[J][i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n, a.K >= V);
+        }
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    load_rows(even, 0);
+    load_rows(odd, 1);
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -227,11 +245,7 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
             *reinterpret_cast<f32x4_t*>(lds + at((wave >> 1) * 32 + 16 * j + (lane & 15),
                                                  (wave & 1) * 16 + 4 * i + (lane >> 4))) = acc[i][j];
     __syncthreads();
-    // four groups of 8 columns a thread, 16 tokens apart
-    constexpr bool ANY = W != Widths::kWhole;
-    const int c = tid % 16, col = k0 + c * 8, n = ANY ? min(V, a.K - col) : V;
     if (col >= a.K) return;
-    const int first = tid / 16;
     float f[4][V];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -241,18 +255,18 @@ __device__ __forceinline__ void router_dx_tile(const RouterBwdArgs& a, const uin
 #pragma unroll
             for (int x = 0; x < 4; ++x) f[i][4 * u + x] = v[x];
         }
-#pragma unroll 2
-    for (int j = 0; j < a.rows; ++j) {
-        u16x8_t r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // (tokens past the last: the last one's, not stored)
-            const size_t t = t0 + min((long)(first + i * 16), rows - 1);
-            r[i] = ld_bf16_bits<ANY, true>(a.dx_rows + (t * a.rows + j) * a.K + col, n, a.K >= V);
-        }
+    auto add_rows = [&](auto at, int j) {
+        constexpr int J = decltype(at)::value;
+        if (j >= a.rows) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int u = 0; u < V; ++u) f[i][u] += bf16_bits_to_f32(r[i][u]);
+            for (int u = 0; u < V; ++u) f[i][u] += bf16_bits_to_f32(row[J][i][u]);
+        load_rows(at, j + 2);
+    };
+    for (int j = 0; j < a.rows; j += 2) {
+        add_rows(even, j);
+        add_rows(odd, j + 1);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
