@@ -93,5 +93,6 @@ def moe_grouped_gemm_dw_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: torc
     dev = codes.device
     _arg(codes, "codes", _I8, (nx, K), dev)
     _arg(scales, "scales", _U8, (nx, _blocks(K)), dev)
-    return _product_dw("moe_grouped_gemm_dw_ckpt", dy, (codes, scales), expert_offsets, sorted_ids, topk,
-                       num_tokens, gather_dy, gather_x, out_dtype, out, accumulate, workspace)
+    return _product_dw("moe_grouped_gemm_dw_ckpt", dev, dy, (codes.data_ptr(), scales.data_ptr()),
+                       codes.shape, expert_offsets, sorted_ids, topk, num_tokens, gather_dy, gather_x,
+                       out_dtype, out, accumulate, workspace)

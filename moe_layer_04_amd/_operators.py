@@ -246,19 +246,19 @@ def moe_grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     moe_grouped_gemm's weights: [E,N,K] in ``out_dtype`` (bf16 or fp32), or
     into ``out``; ``accumulate`` adds to an fp32 ``out``.  gather_dy /
     gather_x: that operand has num_tokens rows, read by the rows' tokens."""
-    nx, K = _sizes(x, "x", 2)
-    _arg(x, "x", _BF16, (nx, K), x.device)
-    return _product_dw("moe_grouped_gemm_dw", dy, (x,), expert_offsets, sorted_ids, topk, num_tokens,
-                       gather_dy, gather_x, out_dtype, out, accumulate, workspace)
+    shape = _sizes(x, "x", 2)
+    dev = x.device
+    _arg(x, "x", _BF16, shape, dev)
+    return _product_dw("moe_grouped_gemm_dw", dev, dy, (x.data_ptr(),), shape, expert_offsets, sorted_ids,
+                       topk, num_tokens, gather_dy, gather_x, out_dtype, out, accumulate, workspace)
 
 
-def _product_dw(fn, dy, x, expert_offsets, sorted_ids, topk, num_tokens, gather_dy, gather_x, out_dtype,
-                out, accumulate, workspace):
-    """x: the tensors that hold it, the first of its shape (checked)."""
-    nx, K = x[0].shape
-    ny, N = _sizes(dy, "dy", 2)
-    dev = x[0].device
-    _arg(dy, "dy", _BF16, (ny, N), dev)
+def _product_dw(fn, dev, dy, x, x_shape, expert_offsets, sorted_ids, topk, num_tokens, gather_dy,
+                gather_x, out_dtype, out, accumulate, workspace):
+    """x: the pointers to what holds it (checked)."""
+    nx, K = x_shape
+    shape = ny, N = _sizes(dy, "dy", 2)
+    _arg(dy, "dy", _BF16, shape, dev)
     if gather_dy and gather_x and ny != nx:
         raise ValueError("two gathered operands must have the same number of rows")
     E = _sizes(expert_offsets, "expert_offsets", 1)[0] - 1
@@ -281,8 +281,8 @@ def _product_dw(fn, dy, x, expert_offsets, sorted_ids, topk, num_tokens, gather_
     out = _out(out, "out", out_dtype, (E, N, K), dev)
     workspace = _workspace(dev, workspace, need, True)
     nbytes = ctypes.c_size_t(workspace.numel())
-    _call(dev, fn, _p(dy), *map(_p, x), _p(expert_offsets), _p(sorted_ids), *sizes, _p(out),
-          _p(workspace), ctypes.byref(nbytes))
+    _call(dev, fn, dy.data_ptr(), *x, expert_offsets.data_ptr(), _p(sorted_ids), *sizes, out.data_ptr(),
+          workspace.data_ptr(), ctypes.byref(nbytes))
     return out
 
 
