@@ -693,7 +693,8 @@ moe_status moe_balance_bwd(const float *dloss, const float *logits, const int32_
  *
  * Errors: as moe_balance, plus INVALID_ARG for K < 1 or rows < 0 and combinations
  * other than those above; UNSUPPORTED for K >= 2^20, rows > 16, M*rows >= 2^28 or
- * 2^24 tiles of dx (64 tokens x 128 columns) and dw or more.
+ * 2^24 tiles of dx (64 tokens x 128 columns) and dw or more, or of 16 tokens (E > 64:
+ * 8, E > 128: 4).
  */
 moe_status moe_topk_bwd(const void *x, const void *w_router, const int32_t *topk_ids,
                         const float *topk_weights, const float *dtopk_weights,

@@ -447,13 +447,19 @@ RouterPlan router_plan(int M, int K, int E) {
     return p;
 }
 
+// tokens of a workgroup of dl's launch: 16 lanes a token up to 64 experts, then 32, 64
+int router_dl_tokens(int E) { return E <= 64 ? 16 : E <= 128 ? 8 : 4; }
+
 size_t parts_bytes(int M, int E) { return ((size_t)kParts * M * router_ep(E) * 2 + 255) / 256 * 256; }
 
 }  // namespace
 
 long router_bwd_workgroups(int M, int K, int E) {
     const RouterPlan p = router_plan(M, K, E);
-    return (long)p.k_tiles * ((M + kSim - 1) / kSim + p.splits * ((E + kSim - 1) / kSim)) + 7;
+    const long products = (long)p.k_tiles * ((M + kSim - 1) / kSim + p.splits * ((E + kSim - 1) / kSim)) + 7;
+    const int tokens = router_dl_tokens(E);
+    const long dl = p.in_place ? 0 : ((long)M + tokens - 1) / tokens;
+    return products > dl ? products : dl;
 }
 
 size_t router_bwd_workspace(int M, int K, int E) {
@@ -468,8 +474,8 @@ void launch_router_bwd(const RouterBwdArgs& a, void* workspace, hipStream_t s) {
     const RouterPlan plan = router_plan(a.M, a.K, a.E);
     if (a.M > 0 && !plan.in_place) {
         auto dl = [&](auto lanes) {
-            constexpr int L = decltype(lanes)::value, tokens = 4 * (kWave / L);
-            const int grid = (a.M + tokens - 1) / tokens;
+            constexpr int L = decltype(lanes)::value;
+            const int tokens = router_dl_tokens(a.E), grid = (a.M + tokens - 1) / tokens;
             if (a.E % 4 == 0) router_dl_kernel<L, true><<<grid, 256, 0, s>>>(a, parts);
             else router_dl_kernel<L, false><<<grid, 256, 0, s>>>(a, parts);
         };

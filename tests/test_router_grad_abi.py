@@ -103,6 +103,19 @@ def test_topk_bwd_refusals(lib):
     overlapping(call, ("dx", "dw", "db"), names[:7], size)
 
 
+@pytest.mark.parametrize("E,tokens", ((1, 16), (64, 16), (65, 8), (128, 8), (129, 4), (256, 4)))
+def test_topk_bwd_tokens_of_a_launch(lib, E, tokens):
+    """The launch for dl takes `tokens` tokens a workgroup of 256 threads and must have
+    fewer than 2^32 threads."""
+    n = ctypes.c_size_t(0)
+
+    def query(M):
+        return lib.moe_topk_bwd(*[None] * 7, 1, M, 8, E, 1, *[None] * 4, ctypes.byref(n), None)
+
+    assert query(tokens * ((1 << 24) - 1)) == OK
+    assert query(tokens * ((1 << 24) - 1) + 1) == UNS
+
+
 def test_python_refuses_host_tensors(lib):
     l, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
     x = torch.zeros(4, 16, dtype=torch.bfloat16)
