@@ -525,7 +525,8 @@ moe_status moe_grouped_plan(int op, int R, int E, int K, int N, moe_product_plan
  *                  and past it stay as they are
  *   a, da          bf16 [R,N];  dg  bf16 [R,2N]
  *   dtopk_weights  out fp32 [slots], or NULL; slots that no row names stay as
- *                  they are
+ *                  they are: zero, if the caller wrote zeros before (their
+ *                  weights changed nothing), which moe_topk_bwd relies on
  *
  * Padding rows are written as zeros.  a and dg must not overlap an input.
  * Errors: INVALID_ARG for null or misaligned pointers, negative sizes, fewer
@@ -677,12 +678,15 @@ moe_status moe_balance_bwd(const float *dloss, const float *logits, const int32_
  *   dw[e]   = sum_t dl[t,e] * x[t],   dbias[e] = sum_t dl[t,e]
  *
  *   x, w_router    as moe_topk
- *   topk_ids, topk_weights, dtopk_weights  [M,topk], or all three NULL; ids
- *                  outside [0,E) pass nothing on
+ *   topk_ids, topk_weights, dtopk_weights  [M,topk], or all three NULL; an id
+ *                  outside [0,E) has no logit to pass its gradient on to, but
+ *                  its w dw is part of the sum over i like every other: dw of
+ *                  a slot that was dropped must be zero
  *   dlogits        fp32 [M,E] (moe_balance_bwd's), or NULL; one of the two is
  *                  needed
  *   dx_rows, rows  bf16 [M*rows,K], a token's rows one after the other
- *                  (moe_grouped_gemm_dx with scatter: rows = topk), or NULL and 0
+ *                  (moe_grouped_gemm_dx with scatter: rows = topk; it leaves rows
+ *                  of dropped slots as they are, which must be zeros), or NULL and 0
  *   dx             out bf16 [M,K]
  *   dw, dbias      out fp32 [E,K] and [E]; dbias may be NULL
  *   workspace      as moe_align_ex; its size depends on (M, K, E)

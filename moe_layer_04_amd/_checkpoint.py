@@ -11,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from ._operators import (_BF16, _arg, _call, _fit, _gated, _new, _out, _p, _product_dw, _sizes)
+from ._operators import (_BF16, _arg, _call, _fit, _gated, _new, _out, _p, _product_dw, _sizes, _weights_grad)
 
 _I8, _U8 = torch.int8, torch.uint8
 
@@ -66,14 +66,14 @@ def moe_silu_mul_bwd_ckpt(da: torch.Tensor, codes: torch.Tensor, scales: torch.T
     """Gradients of moe_silu_mul_ckpt from what it kept: (dg bf16 [R,2N],
     dtopk_weights in topk_weights' shape or None, a bf16 [R,N] -- the forward's
     output from what was kept, which the gradient of the down weights reads -- or
-    None without ``again``).  What moe_silu_mul_bwd leaves unwritten is left so
-    here."""
+    None without ``again``).  Weights of slots that no row names get a gradient of
+    zero; rows at and past num_rows are not written."""
     dev, R, N, slots = _gated(codes, topk_weights, sorted_ids, num_rows, "codes", _I8)
     _fit("moe_silu_mul_bwd_ckpt", R, N, slots)
     _arg(da, "da", _BF16, (R, N), dev)
     _arg(scales, "scales", _U8, (R, 2 * _blocks(N)), dev)
     dg = _new(_BF16, dev, R, 2 * N)
-    dw = None if topk_weights is None else torch.empty_like(topk_weights)
+    dw = _weights_grad(topk_weights, sorted_ids, num_rows)
     a = _new(_BF16, dev, R, N) if again else None
     _call(dev, "moe_silu_mul_bwd_ckpt", _p(da), _p(codes), _p(scales), _p(topk_weights), _p(sorted_ids),
           _p(num_rows), slots, R, N, _p(dg), _p(dw), _p(a))

@@ -307,6 +307,17 @@ def _gated(g, topk_weights, sorted_ids, num_rows, name="g", dtype=_BF16):
     return dev, R, two_n // 2, slots
 
 
+def _weights_grad(topk_weights, sorted_ids, num_rows):
+    """What the gradient of the routing weights is written to, or None.  The kernel
+    writes it for slots that a row names; a weight without a row changed nothing and
+    has a gradient of zero."""
+    if topk_weights is None:
+        return None
+    if sorted_ids is None and num_rows is None:  # every slot has its row
+        return torch.empty_like(topk_weights)
+    return torch.zeros_like(topk_weights)
+
+
 def moe_silu_mul(g: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *,
                  sorted_ids: Optional[torch.Tensor] = None,
                  num_rows: Optional[torch.Tensor] = None,
@@ -329,12 +340,12 @@ def moe_silu_mul_bwd(da: torch.Tensor, g: torch.Tensor,
                      num_rows: Optional[torch.Tensor] = None):
     """Gradients of moe_silu_mul: (dg bf16 [R,2N], dtopk_weights in
     topk_weights' shape, or None without weights).  Weights of slots that no
-    row names get an uninitialised gradient."""
+    row names get a gradient of zero."""
     dev, R, N, slots = _gated(g, topk_weights, sorted_ids, num_rows)
     _fit("moe_silu_mul_bwd", R, N, slots)
     _arg(da, "da", _BF16, (R, N), dev)
     dg = torch.empty_like(g)
-    dw = None if topk_weights is None else torch.empty_like(topk_weights)
+    dw = _weights_grad(topk_weights, sorted_ids, num_rows)
     _call(dev, "moe_silu_mul_bwd", _p(da), _p(g), _p(topk_weights), _p(sorted_ids), _p(num_rows),
           slots, R, N, _p(dg), _p(dw))
     return dg, dw

@@ -89,7 +89,10 @@ def moe_topk_bwd(x: torch.Tensor, w_router: torch.Tensor, topk_ids: Optional[tor
     with topk_ids and topk_weights) and of its logits (dlogits fp32 [M,E]): (dx bf16
     [M,K], dw fp32 [E,K], dbias fp32 [E] or None without ``bias``).  dx_rows bf16
     [M*r,K]: gradients that reach the tokens another way, a token's r rows are
-    added to its dx (moe_grouped_gemm_dx with ``scatter`` leaves them so).
+    added to its dx (moe_grouped_gemm_dx with ``scatter`` leaves them so; where
+    slots are dropped into an ``out`` of zeros, as it writes the others' rows only).
+    A token's dtopk_weights all enter its gradient, also those of ids outside the
+    experts: a dropped slot's is zero, as moe_silu_mul_bwd returns it.
     Without topk_ids, topk_weights and dtopk_weights only dlogits is carried on."""
     M, K = _sizes(x, "x", 2)
     dev = x.device
