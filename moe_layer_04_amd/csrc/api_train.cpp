@@ -66,10 +66,11 @@ moe_status grouped_rows(bool dx, const void* in, const void* w, const int32_t* o
     if (misaligned(in) || misaligned(w) || misaligned(offsets) || misaligned(sorted_ids) ||
         misaligned(out))
         return MOE_ERR_INVALID_ARG;
-    // workgroups read all of an operand while others write
+    // workgroups read all of an operand and of the lists while others write
     const long slots = (long)T * topk, out_bytes = (rows & MOE_ROWS_SCATTER ? slots : R) * (dx ? K : N) * 2;
-    if (overlap(out, out_bytes, in, (rows & MOE_ROWS_GATHER ? (long)T : R) * (dx ? N : K) * 2) ||
-        overlap(out, out_bytes, w, (long)E * N * K * 2))
+    if (overlaps<1, 4>({{out, out_bytes}},
+                       {{in, (rows & MOE_ROWS_GATHER ? (long)T : R) * (dx ? N : K) * 2},
+                        {w, (long)E * N * K * 2}, {offsets, 4L * (E + 1)}, {sorted_ids, 4L * R}}))
         return MOE_ERR_INVALID_ARG;
     const uint32_t how = rows & MOE_ROWS_GATHER ? moe::kRowToken : moe::kRowSorted;
     g.w = (const uint16_t*)w;
@@ -136,9 +137,10 @@ moe_status grouped_dw(const void* dy, const void* x, bool kept, const uint8_t* s
         misaligned(sorted_ids) || misaligned(dw))
         return MOE_ERR_INVALID_ARG;
     const long dw_bytes = (long)E * N * K * (g.out_f32 ? 4 : 2);
-    if (overlap(dw, dw_bytes, dy, (rows & MOE_ROWS_GATHER_DY ? (long)T : R) * N * 2) ||
-        overlap(dw, dw_bytes, x, x_rows * K * (kept ? 1 : 2)) ||
-        (kept && overlap(dw, dw_bytes, scales, x_rows * ckpt_blocks(K))))
+    if (overlaps<1, 5>({{dw, dw_bytes}},
+                       {{dy, (rows & MOE_ROWS_GATHER_DY ? (long)T : R) * N * 2},
+                        {x, x_rows * K * (kept ? 1 : 2)}, {scales, x_rows * ckpt_blocks(K)},
+                        {expert_offsets, 4L * (E + 1)}, {sorted_ids, 4L * R}}))
         return MOE_ERR_INVALID_ARG;
     g.dy = (const uint16_t*)dy;
     if (kept) {
