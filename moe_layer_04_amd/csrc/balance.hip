@@ -10,9 +10,11 @@
 // cost is shared by them.  Both passes are meant to be bound by HBM: the logits are
 // read once, as 16 bytes a lane and group.  Sums are fp32 in a fixed order: a
 // lane's tokens one after the other, then the lanes, the waves and the workgroups;
-// counts are integers.  32768 tokens of 256 experts: forward 8.9 us (35 MB; 13.1 with
-// 64 lanes a token, whose exchanges it then waits for) and 4.2 to join the
-// workgroups, backward 12.4 us (67 MB, 5.4 TB/s).
+// counts are integers.  32768 tokens of 256 experts, a tenth masked, kernel times on
+// average: forward 10.9-11.7 us (35 MB) and 4.7 to join the workgroups, backward 13.4-
+// 15.0 us (67 MB, 4.5-5.0 TB/s); 15.6 and 14.9 us a call in a captured graph.  (With 64
+// lanes a token, whose exchanges it then waits for, the forward took 1.5 times as
+// long.)
 #include "common.hpp"
 #include "launch.hpp"
 

@@ -9,7 +9,7 @@
 // All are bound by HBM: every value is read and written once, 16 bytes of bf16 or
 // 8 of codes a lane; a quad of lanes holds a block.  Arithmetic is fp32.  8192 x
 // 7168: to codes 31.5 us (5.6 TB/s), back 26.3 (6.8); the activation of 8192 x 14336
-// forward 150-158 us (6.0-6.3 TB/s), backward 172-176 (6.7-6.9); rows that are no
+// forward 158-167 us (5.7-6.0 TB/s), backward 176-181 (6.5-6.7); rows that are no
 // multiple of 8 long 4.2-5.4 TB/s.  Codes stay in the L2 (past it the forward took
 // 164 us against 157, ckpt_rows 34.8 against 32.9).
 #include "ckpt.hpp"

@@ -50,7 +50,7 @@ constexpr int kSimAhead = 2;                   // steps loaded ahead
 // The tile of a weight gradient, `rows` x `cols` values of it from `first` on,
 // through LDS: a store instruction writes whole rows of the tile, where the
 // accumulators hold 16 rows of four values (16 rows over 8 experts of 1433 x 4095:
-// 32.7 us against 57.4; 4096 rows, 4097 x 2049: 181 against 221).  Chunks of 16
+// 32.7 us against 57.4; 4096 rows, 4097 x 2049 in bf16: 181 against 221).  Chunks of 16
 // bytes are permuted by the row.
 template <int TILE, bool F32>
 __device__ __forceinline__ void store_grad(char* lds, const f32x4_t (&acc)[TILE / 32][TILE / 32],
@@ -410,8 +410,9 @@ void launch_small_tiles(const GroupedArgs& g, hipStream_t s) {
 //             8x2/8 4095->14337 [904, two rows an expert] 176/192
 //   dx  N->K  2048x2/8 4097->2049 [544] 294/203, 512x2/8 1433->4095 [256] 53.7/48.1,
 //             4097->1025 [72] 59/89
-//   dw  N x K 2048x2/8 4097x2049 [4488] 345/223, 4096x2/8 1025x1025 [648] 101/79,
-//             513x513 [200] 32.5/39.1, 512x2/8 1025x1025 [648] 23.2/23.8
+//   dw  N x K, rows looked up, an even routing, bf16 and fp32: 2048x2/8 4097x2049 [4488]
+//             302/166 and 336/206, 4096x2/8 1025x1025 [648] 92/64 and 90/63, 513x513
+//             [200] 26.6/29.8 and 27.5/31.1, 512x2/8 1025x1025 [648] 20.2/16.8 and 22.7/19.2
 bool wide(const GroupedArgs& g, int op) {
     if (chunked(g) || g.K < 8 || g.N < 8) return false;
     const auto tiles = [](int width) { return (long)((width + 2 * kSim - 1) / (2 * kSim)); };
@@ -609,10 +610,18 @@ size_t grouped_dw_workspace(const GroupedArgs& g) {
     return splits > 1 ? (size_t)splits * g.E * g.N * g.K * 4 : 0;
 }
 // x kept in 8 bits: few small tiles form its values as they store them to LDS, each
-// its own; with more of them a launch that brings the rows back costs less.  us,
-// so / brought back: 666 rows over 8 experts of 1032 x 256 [544 tiles] 9.6/11.0, 1000
-// over 7 of 1001 x 330 [672] 11.2/13.7, 512 of one 512 x 512 [64] 12.6/13.9; 1024 over
-// 8 of 1024 x 1024 [2048] 22.7/20.1, 4096 over 8 of 4097 x 2049 (128 x 128) 356/320
+// its own; with more of them a launch that brings the rows back costs less.  us a
+// call, so / brought back (the same in a captured graph), rows / experts, N x K
+// [tiles, steps]:
+//   666/8 1032x256 [544, 2] 11.2/15.1 (8.8/8.6), 1000/7 1001x330 [672, 3] 11.6/15.1
+//   (9.1/11.4), 1024/8 1024x512 [1024, 2] 17.2/21.7 (12.5/12.4), 1024x640 [1280, 2]
+//   16.0/20.8 (15.5/14.7), 1024x768 [1536, 2] 17.6/21.5 (17.7/15.1), 1024x1024 [2048, 2]
+//   21.5/17.8 (21.9/18.2); 512/1 512x512 [64, 8] 11.7/14.7 (11.7/12.9), 8192/8 513x513
+//   [648, 16] 30.8/33.7, 8192/4 1001x1001 [1024, 32] 73/101, 2048/1 [256, 32] 41/50
+// A hundred steps and more would take the launch as well, which this rule leaves out:
+//   8192/1 1001x1001 [256, 128] 198/176, 509x509 [64, 128] 202/181, 32768/1 333x333
+//   [36, 512] 827/736
+// (128 x 128 tiles read bf16 only: 4096/8 4097x2049 356 with codes, 320.)
 bool grouped_dw_restores(const GroupedArgs& g) {
     return !small_dw(g) || wide(g, kOpDw) || small_workgroups(g, kOpDw, kSim) > 1024;
 }

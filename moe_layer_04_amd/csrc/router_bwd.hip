@@ -12,8 +12,9 @@
 // two (off by at most 2^-16 of a term), dWr three, so nothing of dl is lost in it.
 // Bound by HBM with few experts, with many by the latency of dWr's steps, whose
 // workgroups are few: 4096 tokens of 4096 over 8 experts, two rows a token, 28 us
-// for the products (134 MB), 4 for dl and 4 to join dWr's ranges; of 7168 over 256
-// and eight rows 151 us (587 MB; dx alone 116, dWr alone 60), 6 and 6.
+// for the products (134 MB of operands and results), 4 for dl and 4 to join dWr's
+// ranges; of 7168 over 256 and eight rows 151 us (587 MB of them, 757 by the
+// counters, as x is read by several tiles; dx alone 116, dWr alone 60), 7 and 6.
 #include "launch.hpp"
 #include "rows.hpp"
 #include "small_tiles.hpp"
@@ -375,8 +376,9 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
 }
 
 // Both products in one launch: dWr's tiles, which take long and wait for their steps,
-// first, and dx's, which are bound by HBM, beside and behind them (4096 x 7168 over
-// 256: 163 us a call, dx's first 186).
+// first, and dx's, which are bound by HBM, beside and behind them (us a call, so / dx's
+// first: 4096 x 7168 over 256 157/182, 8192 x 4096 over 64 84/90, 4096 x 4096 over 8
+// 34.2/34.5).
 template <Widths W, bool IN_PLACE>
 __global__ __launch_bounds__(256, 3) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
                                                                  int splits, float* __restrict__ sums, int dw_tiles) {
@@ -437,9 +439,14 @@ RouterPlan router_plan(int M, int K, int E) {
     const int steps = (M + kSim - 1) / kSim;
     const long tiles = (long)((E + kSim - 1) / kSim) * p.k_tiles;
     // Ranges of the tokens up to two workgroups of dWr a CU, while one has four steps
-    // and the whole 12 (a range more is a third launch; whole / in ranges: 512 tokens of
-    // 4096 over 8 13.8/11.7 us of the GPU, 768 18.5/14.2, 1024 24.1/14.5); up to four a
-    // CU: 4096 of 7168 over 256 172 us against 163.
+    // and the whole 12: ranges are a third launch, which costs a stream of calls 2-4 us
+    // on the host.  us a call, whole / in two (the same in a captured graph): 512 tokens
+    // of 4096 over 8 17.2/20.9 (14.2/12.1), 704 18.3/20.8 (18.2/14.5), 768 19.3/20.9
+    // (19.4/15.0), 1024 24.6/20.9 (24.8/18.6); of 1024 over 64 512 18.2/20.4 (14.8/12.9),
+    // 768 19.6/20.4 (19.5/14.7), 1024 24.5/19.7 (24.3/17.4).  So from 8 to 11 steps a
+    // graph pays 2-4 us for what a stream saves, at 12 and 13 the stream one for what
+    // the graph saves; and where the tiles are many, 12 steps are few: 768 of 7168 over
+    // 256 39.4/43.0 (39.6/43.2).  Up to four workgroups a CU: 4096 of these 172 against 163.
     p.splits = 1;
     while (steps >= 12 && p.splits < 64 && tiles * p.splits * 2 <= 512 && steps / (p.splits * 2) >= 4) p.splits *= 2;
     p.dw_tiles = (int)(tiles * p.splits);
