@@ -378,7 +378,9 @@ __device__ __forceinline__ void router_dw_tile(const RouterBwdArgs& a, const uin
 // Both products in one launch: dWr's tiles, which take long and wait for their steps,
 // first, and dx's, which are bound by HBM, beside and behind them (us a call, so / dx's
 // first: 4096 x 7168 over 256 157/182, 8192 x 4096 over 64 84/90, 4096 x 4096 over 8
-// 34.2/34.5).
+// 34.2/34.5).  Three workgroups a CU leave 168 registers: the variants that form dl in
+// place at widths that are no multiples of 8 spill 3 of them, below 8 columns 17 (calls
+// of up to 128 tokens, which wait for the host).
 template <Widths W, bool IN_PLACE>
 __global__ __launch_bounds__(256, 3) void router_products_kernel(RouterBwdArgs a, const uint16_t* __restrict__ parts,
                                                                  int splits, float* __restrict__ sums, int dw_tiles) {
