@@ -231,7 +231,8 @@ def moe_grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, expert_offsets: torch
                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx[i] = w[e]^T dy[i]: the gradient of moe_grouped_gemm's input rows.
     dy bf16 [R,N] (or [num_tokens,N] with ``gather``); returns bf16 [R,K], or
-    [num_tokens*topk,K] with ``scatter``."""
+    [num_tokens*topk,K] with ``scatter``.  Rows of a new output that no sorted
+    row writes are uninitialised."""
     return _product("moe_grouped_gemm_dx", dy, w, expert_offsets, sorted_ids, topk, num_tokens,
                     gather, scatter, out, workspace, True)
 
